@@ -323,6 +323,77 @@ MUSE_API muse_status muse_quantize_nvfp4_rows(const void* src, int64_t rows, int
                                               void* scales, void* stream);
 
 /* ---------------------------------------------------------------------------------
+ * 8-bit integer matrices with one float scale per row (a token's activations, or an output
+ * channel's weights), and their product:
+ *   s_r = max(max_k |x_rk| / 127, 2^-126),  q_rk = x_rk / s_r rounded to nearest, ties to even
+ *   out[t, n] = (sum_k q_tk w_nk) * (s_t * v_n)
+ * max / 127 and x / s are float32 divisions; the sum is exact (K <= 131072), rounded to
+ * float32, multiplied by the float32 product of the scales and rounded to the output type.
+ * A row holding a NaN or an infinity gets scale NaN and codes 0: its products are NaN.
+ * Codes and weights are dense row-major; x and out rows may lie further apart (ld, in
+ * elements). A call with no rows launches nothing.
+ * --------------------------------------------------------------------------------- */
+
+/* Weights of one product: int8 codes [out, in] (device, 16-byte aligned) and float scales
+ * [out] (device). The struct lives in host memory. muse_quantize_int8_rows makes both. */
+typedef struct muse_int8_weight {
+  const void* codes;
+  const float* scales;
+} muse_int8_weight;
+
+/* rows x K values of type dtype (muse_dtype; aligned to their type, row r at src + r * ld) ->
+ * codes int8 [rows, K] (16-byte aligned) and scales float [rows]. K a multiple of 16, at
+ * most 2^20; ld >= K. Enqueued on `stream`. */
+MUSE_API muse_status muse_quantize_int8_rows(const void* src, int32_t dtype, int64_t rows, int64_t K, int64_t ld,
+                                             void* codes, float* scales, void* stream);
+
+/* out[T, N] (out_dtype, row t at out + t * ldo, ldo >= N) from x_codes int8 [T, K] (16-byte
+ * aligned), x_scales float [T] and w (N channels of K codes). K a multiple of 16, at most
+ * 131072; T and N at most 2^24. out may not overlap an input. `status`: optional device
+ * uint32[2], zeroed by the caller, that receives {MUSE_ERR_TIMEOUT, detail} if a bounded
+ * wait of the kernel runs out. */
+MUSE_API muse_status muse_int8_matmul(const void* x_codes, const float* x_scales, int64_t T, int64_t K,
+                                      const muse_int8_weight* w, int64_t N, void* out, int32_t out_dtype, int64_t ldo,
+                                      uint32_t* status, void* stream);
+
+/* The same from float rows: x [T, K] of type x_dtype (row t at x + t * ldx) is quantised as by
+ * muse_quantize_int8_rows, then multiplied; bit for bit the two calls one after the other.
+ * The workspace (device, 256-byte aligned, muse_int8_linear_workspace_size bytes) holds the
+ * codes and scales; calls whose work overlaps need workspaces of their own. */
+MUSE_API muse_status muse_int8_linear_workspace_size(int64_t T, int64_t K, size_t* bytes);
+MUSE_API muse_status muse_int8_linear(const void* x, int32_t x_dtype, int64_t T, int64_t K, int64_t ldx,
+                                      const muse_int8_weight* w, int64_t N, void* out, int32_t out_dtype, int64_t ldo,
+                                      void* workspace, size_t workspace_bytes, uint32_t* status, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * The whole layer for a few tokens (cfg->T <= MUSE_FEW_TOKENS) in one kernel: the mathematics
+ * of muse_latent_moe_forward with the same arguments and options, for interactive decoding,
+ * where the launches of the forward cost more than their work. It differs in rounding only:
+ * expert outputs and the sublayer's f stay FP32, float32 workloads multiply in FP32 (not
+ * TF32), and with NVFP4 experts the latent is rounded to f16 once. It requires 16-bit or
+ * float32 activations (MUSE_ACT_NVFP4 is UNSUPPORTED); NVFP4 experts require L and I
+ * multiples of 256. stage_events is ignored. cfg->workspace: device, 256-byte aligned,
+ * muse_latent_moe_few_tokens_workspace_size bytes, a layout of its own; calls whose work
+ * overlaps on the GPU need workspaces of their own. The kernel is launched cooperatively
+ * (its CTAs, one per SM, wait for one another): MUSE_ERR_CUDA where the device cannot hold
+ * them at once. Its waits are bounded; muse_latent_moe_few_tokens_status synchronises `stream`
+ * and returns the status word of the last call on this workspace.
+ * The _checked form takes every tensor by its shape, as muse_latent_moe_forward_checked. */
+#define MUSE_FEW_TOKENS 8
+MUSE_API muse_status muse_latent_moe_few_tokens_workspace_size(const muse_moe_config* cfg, size_t* bytes);
+MUSE_API muse_status muse_latent_moe_few_tokens(const muse_moe_config* cfg, const void* x, const void* W_router,
+                                                const void* W_pool, const void* W_gate, const void* W_up,
+                                                const void* W_down, const void* gamma, const void* W_unpool,
+                                                void* out, void* stream);
+MUSE_API muse_status muse_latent_moe_few_tokens_checked(const muse_moe_config* cfg, const muse_tensor* x,
+                                                        const muse_tensor* W_router, const muse_tensor* W_pool,
+                                                        const muse_tensor* W_gate, const muse_tensor* W_up,
+                                                        const muse_tensor* W_down, const muse_tensor* gamma,
+                                                        const muse_tensor* W_unpool, const muse_tensor* out,
+                                                        void* stream);
+MUSE_API muse_status muse_latent_moe_few_tokens_status(const muse_moe_config* cfg, void* stream, uint32_t* detail);
+
+/* ---------------------------------------------------------------------------------
  * Expert parallelism (EP) over G ranks (Muse Spark Open deep dive, §4.3: the two expert
  * tensors split along the expert dimension, the latent rows moved to the experts' ranks
  * and back, the norm weights replicated; on each rank the local experts see every row

@@ -29,10 +29,16 @@ EXPORTS = ("muse_moe_config_init", "muse_latent_moe_workspace_size", "muse_laten
            "muse_status_string", "muse_latent_moe_launch_count", "muse_latent_moe_forward_static_scratch",
            "muse_selftest_bounded_wait", "muse_quantize_nvfp4_rows", "muse_latent_moe_forward_host_batches",
            "muse_ep_workspace_layout", "muse_ep_dispatch", "muse_ep_experts", "muse_ep_combine",
-           "muse_latent_moe_forward_checked", "muse_latent_moe_stage_name", "muse_last_cuda_error")
+           "muse_latent_moe_forward_checked", "muse_latent_moe_stage_name", "muse_last_cuda_error",
+           "muse_quantize_int8_rows", "muse_int8_matmul", "muse_int8_linear_workspace_size", "muse_int8_linear",
+           "muse_latent_moe_few_tokens_workspace_size", "muse_latent_moe_few_tokens",
+           "muse_latent_moe_few_tokens_checked", "muse_latent_moe_few_tokens_status")
 
 # roles of an expert-parallel workspace (muse_ep_role)
 EP_HOME, EP_EXPERTS = 1, 2
+
+# most tokens of a muse_latent_moe_few_tokens call (MUSE_FEW_TOKENS)
+FEW_TOKENS = 8
 
 # size of the library's built-in scratch array (MUSE_STATIC_SCRATCH_BYTES)
 STATIC_SCRATCH_BYTES = 16 << 20
@@ -86,6 +92,10 @@ def tensor_desc(t) -> Tensor:
 
 class Nvfp4Weight(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("block_scales", ctypes.c_void_p), ("matrix_scale", ctypes.c_void_p)]
+
+
+class Int8Weight(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 class WorkspaceLayout(ctypes.Structure):
@@ -145,6 +155,23 @@ def lib() -> ctypes.CDLL:
         L.muse_latent_moe_stage_name.restype = ctypes.c_char_p
         L.muse_latent_moe_launch_count.argtypes = [cp]
         L.muse_latent_moe_launch_count.restype = ctypes.c_int32
+        wp = ctypes.POINTER(Int8Weight)
+        L.muse_quantize_int8_rows.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+        L.muse_quantize_int8_rows.restype = ctypes.c_int
+        L.muse_int8_matmul.argtypes = [vp, vp, i64, i64, wp, i64, vp, i32, i64, vp, vp]
+        L.muse_int8_matmul.restype = ctypes.c_int
+        L.muse_int8_linear_workspace_size.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_size_t)]
+        L.muse_int8_linear_workspace_size.restype = ctypes.c_int
+        L.muse_int8_linear.argtypes = [vp, i32, i64, i64, i64, wp, i64, vp, i32, i64, vp, ctypes.c_size_t, vp, vp]
+        L.muse_int8_linear.restype = ctypes.c_int
+        L.muse_latent_moe_few_tokens_workspace_size.argtypes = [cp, ctypes.POINTER(ctypes.c_size_t)]
+        L.muse_latent_moe_few_tokens_workspace_size.restype = ctypes.c_int
+        L.muse_latent_moe_few_tokens.argtypes = [cp] + [vp] * 10
+        L.muse_latent_moe_few_tokens.restype = ctypes.c_int
+        L.muse_latent_moe_few_tokens_checked.argtypes = [cp] + [ctypes.POINTER(Tensor)] * 9 + [vp]
+        L.muse_latent_moe_few_tokens_checked.restype = ctypes.c_int
+        L.muse_latent_moe_few_tokens_status.argtypes = [cp, vp, ctypes.POINTER(ctypes.c_uint32)]
+        L.muse_latent_moe_few_tokens_status.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -229,6 +256,12 @@ def forward_checked(cfg: Config, x, W_router, W_pool, W_gate, W_up, W_down, gamm
     """Enqueue one forward through the shape-checked entry point: every argument is a torch
     tensor (NVFP4 experts: a (codes, block scales, matrix scales) triple each) described by
     its dtype, shape and strides; the library rejects a mismatch before launching anything."""
+    _call_checked(lib().muse_latent_moe_forward_checked, "muse_latent_moe_forward_checked", cfg, x, W_router, W_pool,
+                  W_gate, W_up, W_down, gamma, W_unpool, out, stream)
+
+
+def _call_checked(fn, name: str, cfg: Config, x, W_router, W_pool, W_gate, W_up, W_down, gamma, W_unpool, out,
+                  stream) -> None:
     def one(t):
         return ctypes.byref(tensor_desc(t))
 
@@ -239,9 +272,30 @@ def forward_checked(cfg: Config, x, W_router, W_pool, W_gate, W_up, W_down, gamm
         d = tensor_desc(t)
         return ctypes.pointer(d), d
     eg, eu, ed = expert(W_gate), expert(W_up), expert(W_down)
-    code = lib().muse_latent_moe_forward_checked(ctypes.byref(cfg), one(x), one(W_router), one(W_pool), eg[0], eu[0],
-                                                 ed[0], one(gamma), one(W_unpool), one(out), _stream_handle(stream))
-    _check(code, "muse_latent_moe_forward_checked")
+    code = fn(ctypes.byref(cfg), one(x), one(W_router), one(W_pool), eg[0], eu[0], ed[0], one(gamma), one(W_unpool),
+              one(out), _stream_handle(stream))
+    _check(code, name)
+
+
+def few_tokens_workspace_size(cfg: Config) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().muse_latent_moe_few_tokens_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "muse_latent_moe_few_tokens_workspace_size")
+    return int(n.value)
+
+
+def few_tokens(cfg: Config, x, W_router, W_pool, W_gate, W_up, W_down, gamma, W_unpool, out, stream=None) -> None:
+    """Enqueue the whole layer for cfg.T <= FEW_TOKENS tokens as one kernel, every tensor checked
+    by its shape as in forward_checked; cfg.workspace: few_tokens_workspace_size(cfg) bytes."""
+    _call_checked(lib().muse_latent_moe_few_tokens_checked, "muse_latent_moe_few_tokens_checked", cfg, x, W_router,
+                  W_pool, W_gate, W_up, W_down, gamma, W_unpool, out, stream)
+
+
+def few_tokens_status(cfg: Config, stream=None):
+    """(status, detail) of the last few_tokens call on cfg.workspace; synchronises the stream."""
+    detail = ctypes.c_uint32(0)
+    code = lib().muse_latent_moe_few_tokens_status(ctypes.byref(cfg), _stream_handle(stream), ctypes.byref(detail))
+    return int(code), int(detail.value)
 
 
 def forward_static_scratch(cfg: Config, x, W_router, W_pool, W_gate, W_up, W_down, gamma, W_unpool, out,
@@ -337,6 +391,116 @@ def quantize_nvfp4_rows(src, codes, scales, stream=None) -> None:
                                           _stream_handle(stream)), "muse_quantize_nvfp4_rows")
 
 
+def _rows(t, name: str):
+    """Pointer, muse_dtype and row distance of a 2-D float tensor whose rows are contiguous."""
+    import torch
+    if t.dim() != 2 or t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name} must be a 2-D float32 or bfloat16 tensor")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    ld = int(t.stride(0)) if rows > 1 else int(cols)
+    return int(t.data_ptr()), (MUSE_F32 if t.dtype == torch.float32 else MUSE_BF16), ld
+
+
+def _int8_operand(codes, scales, name: str):
+    import torch
+    if codes.dim() != 2 or codes.dtype != torch.int8 or not codes.is_contiguous():
+        raise ValueError(f"{name} codes must be a contiguous 2-D int8 tensor")
+    if scales.shape != (codes.shape[0],) or scales.dtype != torch.float32 or not scales.is_contiguous():
+        raise ValueError(f"{name} scales must be a contiguous float32 tensor with one value per row of the codes")
+
+
+def _one_device(*tensors):
+    """The device all tensors are on (a context in which the library's calls run)."""
+    import torch
+    dev = tensors[0].device
+    if dev.type != "cuda" or any(t.device != dev for t in tensors):
+        raise ValueError("tensors must be on one CUDA device")
+    return torch.cuda.device(dev)
+
+
+def quantize_int8_rows(src, codes=None, scales=None, stream=None):
+    """src [rows, K] float32 or bfloat16 (rows may lie apart, K a multiple of 16) -> codes int8
+    [rows, K] and scales float32 [rows], created if not given; returns both. For activations a
+    row is a token, for weights [out, in] an output channel."""
+    import torch
+    ptr, dtype, ld = _rows(src, "src")
+    rows, K = src.shape
+    codes = torch.empty((rows, K), dtype=torch.int8, device=src.device) if codes is None else codes
+    scales = torch.empty(rows, dtype=torch.float32, device=src.device) if scales is None else scales
+    _int8_operand(codes, scales, "int8")
+    if codes.shape != src.shape:
+        raise ValueError("codes must have the shape of src")
+    with _one_device(src, codes, scales):
+        _check(lib().muse_quantize_int8_rows(ptr, dtype, int(rows), int(K), ld, _ptr(codes), _ptr(scales),
+                                             _stream_handle(stream)), "muse_quantize_int8_rows")
+    return codes, scales
+
+
+class Int8Linear:
+    """A product with int8 weights: codes [out, in] and scales [out] (quantize_int8_rows of the
+    weights), for up to T_max rows per call. Holds the workspace of the quantised rows, so calls
+    that overlap on the GPU need holders of their own."""
+
+    def __init__(self, codes, scales, T_max: int):
+        import torch
+        _int8_operand(codes, scales, "weight")
+        self.codes, self.scales, self.T_max = codes, scales, int(T_max)
+        self.N, self.K = (int(n) for n in codes.shape)
+        self.weight = Int8Weight(_ptr(codes), _ptr(scales))
+        n = ctypes.c_size_t(0)
+        _check(lib().muse_int8_linear_workspace_size(self.T_max, self.K, ctypes.byref(n)),
+               "muse_int8_linear_workspace_size")
+        with _one_device(codes, scales):
+            self.workspace = torch.empty(max(int(n.value), 1), dtype=torch.uint8, device=codes.device)
+            self.status = torch.zeros(2, dtype=torch.int32, device=codes.device)
+
+    def _out(self, T, out, out_dtype, device):
+        import torch
+        if out is None:
+            out = torch.empty((T, self.N), dtype=out_dtype, device=device)
+        elif tuple(out.shape) != (T, self.N) or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out must be [{T}, {self.N}] of the output type")
+        return (out,) + _rows(out, "out")
+
+    def __call__(self, x, out=None, out_dtype=None, stream=None):
+        """out[T, out] = x[T, in] W^T, x quantised per row; out in x's type unless given."""
+        ptr, dtype, ld = _rows(x, "x")
+        T = int(x.shape[0])
+        if x.shape[1] != self.K:
+            raise ValueError(f"x has {x.shape[1]} columns, the weights {self.K}")
+        if T > self.T_max:
+            raise ValueError(f"T={T} exceeds T_max={self.T_max}")
+        out, optr, odtype, ldo = self._out(T, out, out_dtype or (x.dtype if out is None else None), x.device)
+        with _one_device(x, out, self.codes):
+            _check(lib().muse_int8_linear(ptr, dtype, T, self.K, ld, ctypes.byref(self.weight), self.N, optr, odtype,
+                                          ldo, _ptr(self.workspace), self.workspace.numel(), _ptr(self.status),
+                                          _stream_handle(stream)), "muse_int8_linear")
+        return out
+
+    def matmul(self, x_codes, x_scales, out=None, out_dtype=None, stream=None):
+        """The product of rows that are quantised already (bfloat16 unless out or out_dtype says
+        otherwise); any number of rows."""
+        import torch
+        _int8_operand(x_codes, x_scales, "x")
+        T = int(x_codes.shape[0])
+        if x_codes.shape[1] != self.K:
+            raise ValueError(f"x has {x_codes.shape[1]} columns, the weights {self.K}")
+        out, optr, odtype, ldo = self._out(T, out, out_dtype or (torch.bfloat16 if out is None else None),
+                                           x_codes.device)
+        with _one_device(x_codes, x_scales, out, self.codes):
+            _check(lib().muse_int8_matmul(_ptr(x_codes), _ptr(x_scales), T, self.K, ctypes.byref(self.weight), self.N,
+                                          optr, odtype, ldo, _ptr(self.status), _stream_handle(stream)),
+                   "muse_int8_matmul")
+        return out
+
+    def device_status(self):
+        """(status, detail) that bounded waits of this holder's calls recorded; synchronises."""
+        code, detail = self.status.tolist()
+        return int(code), int(detail) & 0xffffffff
+
+
 def selftest_bounded_wait(limit_ns: int, status_dev, stream=None) -> None:
     """Run the device-side bounded-wait self-test (status_dev: zeroed CUDA int32[2])."""
     _check(lib().muse_selftest_bounded_wait(int(limit_ns), _ptr(status_dev), _stream_handle(stream)),
@@ -413,6 +577,15 @@ class LatentMoE:
         cfg = self.config(T_max)
         self.workspace = torch.empty(workspace_size(cfg), dtype=torch.uint8, device=weights["W_router"].device)
         self.T_max = T_max
+        # the single-kernel form for a few tokens has a (small) workspace of its own; None where the
+        # library does not offer it for these modes
+        self.few_workspace = None
+        try:
+            few = few_tokens_workspace_size(self.config(min(T_max, FEW_TOKENS)))
+            self.few_workspace = torch.empty(few, dtype=torch.uint8, device=weights["W_router"].device)
+        except MuseError as e:
+            if e.code != 2:  # MUSE_ERR_UNSUPPORTED
+                raise
 
     def config(self, T: int, workspace=None) -> Config:
         return block_config(T, self.dims, self.dtype, self.modes, self.w, self.nvfp4, workspace)
@@ -431,4 +604,24 @@ class LatentMoE:
             out = torch.empty((T, self.dims["D"]), dtype=x.dtype, device=x.device)
         w = self.w
         forward_checked(cfg, x, w["W_router"], w["W_pool"], *self.experts, w["gamma"], w["W_unpool"], out, stream)
+        return out
+
+    def few_tokens(self, x, out=None, stream=None, topk_idx=None, topk_w=None):
+        """The layer for 1 .. FEW_TOKENS tokens as one kernel (muse_latent_moe_few_tokens): the same
+        mathematics as calling the holder, for interactive decoding. Calls that overlap on the GPU
+        need holders of their own."""
+        import torch
+        T = x.shape[0]
+        if T > min(self.T_max, FEW_TOKENS):
+            raise ValueError(f"T={T} exceeds {min(self.T_max, FEW_TOKENS)}")
+        for t, dtype in ((topk_idx, torch.int32), (topk_w, torch.float32)):
+            if t is not None and (t.shape != (T, self.dims["k"]) or t.dtype != dtype or t.device != x.device):
+                raise ValueError(f"topk_idx and topk_w are [{T}, {self.dims['k']}] int32 and float32 on x's device")
+        w = self.w
+        with _one_device(x, w["W_router"]):
+            cfg = self.config(T, self.few_workspace)
+            cfg.topk_idx_out, cfg.topk_w_out = _ptr(topk_idx), _ptr(topk_w)
+            if out is None:
+                out = torch.empty((T, self.dims["D"]), dtype=x.dtype, device=x.device)
+            few_tokens(cfg, x, w["W_router"], w["W_pool"], *self.experts, w["gamma"], w["W_unpool"], out, stream)
         return out

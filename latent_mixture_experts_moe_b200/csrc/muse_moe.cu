@@ -19,11 +19,13 @@
 #include <mutex>
 
 #include "muse_moe.h"
+#include "few_tokens.cuh"
 #include "gemm_umma.cuh"
 #include "gemm_umma_2sm.cuh"
 #include "gemm_umma_fp4.cuh"
 #include "gemm_umma_w4a4.cuh"
 #include "gemv_fp4.cuh"
+#include "int8_rows.cuh"
 #include "nvfp4_act.cuh"
 #include "route_kernels.cuh"
 
@@ -1096,6 +1098,193 @@ bool expert_tensor_is(const muse_moe_config& c, const muse_tensor* t, int64_t ro
   return true;
 }
 
+// The expert weights as the forward takes them, from their descriptors.
+struct ExpertOperands {
+  muse_nvfp4_weight q[3];
+  const void *gate, *up, *down;
+};
+
+// Every tensor of a forward against the configuration (see muse_latent_moe_forward_checked).
+muse_status check_tensors(const muse_moe_config& c, const muse_tensor* x, const muse_tensor* W_router,
+                          const muse_tensor* W_pool, const muse_tensor* W_gate, const muse_tensor* W_up,
+                          const muse_tensor* W_down, const muse_tensor* gamma, const muse_tensor* W_unpool,
+                          const muse_tensor* out, ExpertOperands* e) {
+  const int32_t a = c.dtype;  // MUSE_F32 / MUSE_BF16 equal MUSE_ELEM_F32 / MUSE_ELEM_BF16
+  if (!tensor_is(x, a, {c.T, c.D}) || !tensor_is(W_router, a, {c.E, c.D}) || !tensor_is(W_pool, a, {c.L, c.D}) ||
+      !tensor_is(W_unpool, a, {c.D, c.L}) || !tensor_is(out, a, {c.T, c.D}))
+    return MUSE_ERR_INVALID_ARG;
+  if (!(c.gamma_shared ? tensor_is(gamma, a, {c.L}) : tensor_is(gamma, a, {c.E, c.L}))) return MUSE_ERR_INVALID_ARG;
+  if (!expert_tensor_is(c, W_gate, c.I, c.L, &e->q[0], &e->gate) ||
+      !expert_tensor_is(c, W_up, c.I, c.L, &e->q[1], &e->up) ||
+      !expert_tensor_is(c, W_down, c.L, c.I, &e->q[2], &e->down))
+    return MUSE_ERR_INVALID_ARG;
+  const muse_tensor* inputs[] = {x, W_router, W_pool, gamma, W_unpool};
+  for (const muse_tensor* t : inputs)
+    if (overlaps(out, t)) return MUSE_ERR_INVALID_ARG;
+  const int n_exp = c.expert_weights == MUSE_EXPERTS_NVFP4 ? 3 : 1;
+  const muse_tensor* experts[] = {W_gate, W_up, W_down};
+  for (const muse_tensor* t : experts)
+    for (int i = 0; i < n_exp; ++i)
+      if (overlaps(out, &t[i])) return MUSE_ERR_INVALID_ARG;
+  return MUSE_OK;
+}
+
+// ---------------------------------------------------------------------- a few tokens
+// Workspace of muse_latent_moe_few_tokens: status word and barrier counter (one 256-byte
+// block, zeroed by every call), then the intermediates.
+struct FewLayout {
+  size_t logits, xn, z, h, y, ss, c, f, ssf, total;
+};
+
+muse_status validate_few(const muse_moe_config* c) {
+  MUSE_TRY(validate_sizes(c));
+  if (c->T > kFewTokens || c->act_format != MUSE_ACT_BF16) return MUSE_ERR_UNSUPPORTED;
+  if (c->expert_weights == MUSE_EXPERTS_NVFP4 && (c->L % 256 != 0 || c->I % 256 != 0)) return MUSE_ERR_UNSUPPORTED;
+  return MUSE_OK;
+}
+
+FewLayout few_layout(const muse_moe_config& c) {
+  FewLayout l{};
+  const size_t as = act_size(c), T = c.T, A = c.T * c.top_k;
+  const bool finish = c.ffn_post_gain != nullptr || c.residual_gate != nullptr;
+  size_t o = kAlign;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes, kAlign);
+    return at;
+  };
+  l.logits = take(sizeof(float) * T * c.E);
+  l.xn = take(c.ffn_pre_gain != nullptr ? as * T * c.D : 0);
+  l.z = take(as * T * c.L);
+  l.h = take(as * A * c.I);
+  l.y = take(sizeof(float) * A * c.L);
+  l.ss = take(sizeof(float) * A * kFewGridMax);
+  l.c = take(as * T * c.L);
+  l.f = take(finish ? sizeof(float) * T * c.D : 0);
+  l.ssf = take(finish ? sizeof(float) * T * kFewGridMax : 0);
+  l.total = o;
+  return l;
+}
+
+template <typename TA, bool FP4>
+muse_status launch_few(FewArgs& a, cudaStream_t st) {
+  auto kern = k_few_tokens<TA, FP4>;
+  const int grid = std::min(sm_count(), kFewGridMax);
+  void* args[] = {&a};
+  MUSE_CK(cudaMemsetAsync(a.status, 0, kAlign, st));
+  MUSE_CK(cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kern), dim3(grid), dim3(kFewThreads), args, 0, st));
+  return MUSE_OK;
+}
+
+muse_status few_tokens_impl(const muse_moe_config& c, const void* x, const void* W_router, const void* W_pool,
+                            const void* W_gate, const void* W_up, const void* W_down, const void* gamma,
+                            const void* W_unpool, void* out, cudaStream_t st) {
+  const FewLayout l = few_layout(c);
+  uint8_t* ws = static_cast<uint8_t*>(c.workspace);
+  FewArgs a{};
+  a.T = static_cast<int>(c.T);
+  a.D = static_cast<int>(c.D);
+  a.L = static_cast<int>(c.L);
+  a.I = static_cast<int>(c.I);
+  a.E = static_cast<int>(c.E);
+  a.k = c.top_k;
+  a.router_mode = c.router_mode;
+  a.norm_mode = c.norm_mode;
+  a.gamma_shared = c.gamma_shared;
+  a.eps = c.eps;
+  a.logit_scale = c.router_logit_scale;
+  a.rsf = c.routed_scaling;
+  a.pre_norm_eps = c.pre_norm_eps;
+  a.ffn_pre_eps = c.ffn_pre_eps;
+  a.ffn_post_eps = c.ffn_post_eps;
+  a.inv_temp = c.residual_gate != nullptr ? 1.0f / c.residual_gate_temperature : 0.0f;
+  a.gate_eps = c.residual_gate_eps;
+  a.x = x;
+  a.W_router = W_router;
+  a.W_pool = W_pool;
+  a.gamma = gamma;
+  a.W_unpool = W_unpool;
+  a.router_bias = c.router_bias;
+  a.pre_norm_gain = c.pre_norm_gain;
+  a.ffn_pre_gain = c.ffn_pre_gain;
+  a.ffn_post_gain = c.ffn_post_gain;
+  a.residual_gate = c.residual_gate;
+  a.out = out;
+  a.idx_out = c.topk_idx_out;
+  a.w_out = c.topk_w_out;
+  a.status = reinterpret_cast<uint32_t*>(ws);
+  a.barrier = reinterpret_cast<uint32_t*>(ws + 128);
+  a.logits = reinterpret_cast<float*>(ws + l.logits);
+  a.y = reinterpret_cast<float*>(ws + l.y);
+  a.ss = reinterpret_cast<float*>(ws + l.ss);
+  a.f = reinterpret_cast<float*>(ws + l.f);
+  a.ssf = reinterpret_cast<float*>(ws + l.ssf);
+  a.xn = ws + l.xn;
+  a.z = ws + l.z;
+  a.h = ws + l.h;
+  a.c = ws + l.c;
+  if (c.expert_weights == MUSE_EXPERTS_NVFP4) {
+    const muse_nvfp4_weight* g = static_cast<const muse_nvfp4_weight*>(W_gate);
+    const muse_nvfp4_weight* u = static_cast<const muse_nvfp4_weight*>(W_up);
+    const muse_nvfp4_weight* d = static_cast<const muse_nvfp4_weight*>(W_down);
+    a.W_gate = g->codes;
+    a.W_up = u->codes;
+    a.W_down = d->codes;
+    a.s_gate = static_cast<const uint8_t*>(g->block_scales);
+    a.s_up = static_cast<const uint8_t*>(u->block_scales);
+    a.s_down = static_cast<const uint8_t*>(d->block_scales);
+    a.m_gate = g->matrix_scale;
+    a.m_up = u->matrix_scale;
+    a.m_down = d->matrix_scale;
+    return launch_few<__nv_bfloat16, true>(a, st);
+  }
+  a.W_gate = W_gate;
+  a.W_up = W_up;
+  a.W_down = W_down;
+  return c.dtype == MUSE_BF16 ? launch_few<__nv_bfloat16, false>(a, st) : launch_few<float, false>(a, st);
+}
+
+// ---------------------------------------------------------------------- int8 products
+bool aligned_to(const void* p, size_t a) { return p != nullptr && reinterpret_cast<uintptr_t>(p) % a == 0; }
+size_t dtype_size(int32_t dtype) { return dtype == MUSE_BF16 ? 2 : 4; }
+bool valid_dtype(int32_t dtype) { return dtype == MUSE_F32 || dtype == MUSE_BF16; }
+
+muse_status quantize_int8(const void* src, int32_t dtype, int64_t rows, int64_t K, int64_t ld, void* codes,
+                          float* scales, cudaStream_t st) {
+  const int grid = static_cast<int>(std::min<int64_t>(rows, 16 * sm_count()));
+  if (dtype == MUSE_BF16)
+    k_quant_rows_int8<<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(src), ld, static_cast<int>(rows),
+                                            static_cast<int>(K), static_cast<int8_t*>(codes), scales);
+  else
+    k_quant_rows_int8<<<grid, 256, 0, st>>>(static_cast<const float*>(src), ld, static_cast<int>(rows),
+                                            static_cast<int>(K), static_cast<int8_t*>(codes), scales);
+  MUSE_CK(cudaGetLastError());
+  return MUSE_OK;
+}
+
+template <typename TOut>
+muse_status int8_product(const void* xc, const float* xs, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
+                         void* out, int64_t ldo, uint32_t* status, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(cdiv(N, 8)), static_cast<unsigned>(std::min<int64_t>(cdiv(T, 8), 65535)));
+  k_int8_matmul<TOut><<<grid, 256, 0, st>>>(static_cast<const int8_t*>(xc), xs, static_cast<int>(T),
+                                            static_cast<int>(K), static_cast<const int8_t*>(w.codes), w.scales,
+                                            static_cast<int>(N), static_cast<TOut*>(out), ldo);
+  MUSE_CK(cudaGetLastError());
+  return MUSE_OK;
+}
+
+// the sizes, weights and output of an int8 product
+muse_status validate_int8(int64_t T, int64_t K, const muse_int8_weight* w, int64_t N, const void* out,
+                          int32_t out_dtype, int64_t ldo, const uint32_t* status) {
+  if (T < 0 || K < 16 || K % 16 != 0 || N < 1 || ldo < N || !valid_dtype(out_dtype)) return MUSE_ERR_INVALID_ARG;
+  if (w == nullptr || !aligned_to(w->codes, 16) || !aligned_to(w->scales, 4) ||
+      (T > 0 && !aligned_to(out, dtype_size(out_dtype))) || (reinterpret_cast<uintptr_t>(status) & 3u))
+    return MUSE_ERR_INVALID_ARG;
+  if (K > 131072 || T > (int64_t(1) << 24) || N > (int64_t(1) << 24) || ldo > (int64_t(1) << 40))
+    return MUSE_ERR_UNSUPPORTED;
+  return MUSE_OK;
+}
+
 // Scratch for muse_latent_moe_forward_static_scratch: a fixed array in device global
 // memory, so that entry point never allocates. In host code this name stands for the
 // symbol, not a device address; the address comes from cudaGetSymbolAddress.
@@ -1186,26 +1375,9 @@ muse_status muse_latent_moe_forward_checked(const muse_moe_config* cfg, const mu
                                             const muse_tensor* W_down, const muse_tensor* gamma,
                                             const muse_tensor* W_unpool, const muse_tensor* out, void* stream) {
   MUSE_TRY(validate_sizes(cfg));
-  const muse_moe_config& c = *cfg;
-  const int32_t a = c.dtype;  // MUSE_F32 / MUSE_BF16 equal MUSE_ELEM_F32 / MUSE_ELEM_BF16
-  if (!tensor_is(x, a, {c.T, c.D}) || !tensor_is(W_router, a, {c.E, c.D}) || !tensor_is(W_pool, a, {c.L, c.D}) ||
-      !tensor_is(W_unpool, a, {c.D, c.L}) || !tensor_is(out, a, {c.T, c.D}))
-    return MUSE_ERR_INVALID_ARG;
-  if (!(c.gamma_shared ? tensor_is(gamma, a, {c.L}) : tensor_is(gamma, a, {c.E, c.L}))) return MUSE_ERR_INVALID_ARG;
-  muse_nvfp4_weight qg{}, qu{}, qd{};
-  const void *wg = nullptr, *wu = nullptr, *wd = nullptr;
-  if (!expert_tensor_is(c, W_gate, c.I, c.L, &qg, &wg) || !expert_tensor_is(c, W_up, c.I, c.L, &qu, &wu) ||
-      !expert_tensor_is(c, W_down, c.L, c.I, &qd, &wd))
-    return MUSE_ERR_INVALID_ARG;
-  const muse_tensor* inputs[] = {x, W_router, W_pool, gamma, W_unpool};
-  for (const muse_tensor* t : inputs)
-    if (overlaps(out, t)) return MUSE_ERR_INVALID_ARG;
-  const int n_exp = c.expert_weights == MUSE_EXPERTS_NVFP4 ? 3 : 1;
-  const muse_tensor* experts[] = {W_gate, W_up, W_down};
-  for (const muse_tensor* t : experts)
-    for (int i = 0; i < n_exp; ++i)
-      if (overlaps(out, &t[i])) return MUSE_ERR_INVALID_ARG;
-  return muse_latent_moe_forward(cfg, x->data, W_router->data, W_pool->data, wg, wu, wd, gamma->data,
+  ExpertOperands e;
+  MUSE_TRY(check_tensors(*cfg, x, W_router, W_pool, W_gate, W_up, W_down, gamma, W_unpool, out, &e));
+  return muse_latent_moe_forward(cfg, x->data, W_router->data, W_pool->data, e.gate, e.up, e.down, gamma->data,
                                  W_unpool->data, const_cast<void*>(out->data), stream);
 }
 
@@ -1399,6 +1571,94 @@ muse_status muse_quantize_nvfp4_rows(const void* src, int64_t rows, int64_t K, v
       nullptr, nullptr, static_cast<int>(rows), static_cast<const __nv_bfloat16*>(src), static_cast<int>(K),
       static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
   return cudaGetLastError() == cudaSuccess ? MUSE_OK : MUSE_ERR_CUDA;
+}
+
+muse_status muse_quantize_int8_rows(const void* src, int32_t dtype, int64_t rows, int64_t K, int64_t ld, void* codes,
+                                    float* scales, void* stream) {
+  if (!valid_dtype(dtype) || rows < 0 || K < 16 || K % 16 != 0 || ld < K) return MUSE_ERR_INVALID_ARG;
+  if (rows > (int64_t(1) << 30) || K > (int64_t(1) << 20) || ld > (int64_t(1) << 40)) return MUSE_ERR_UNSUPPORTED;
+  if (rows == 0) return MUSE_OK;
+  if (!aligned_to(src, dtype_size(dtype)) || !aligned_to(codes, 16) || !aligned_to(scales, 4))
+    return MUSE_ERR_INVALID_ARG;
+  return quantize_int8(src, dtype, rows, K, ld, codes, scales, static_cast<cudaStream_t>(stream));
+}
+
+muse_status muse_int8_matmul(const void* x_codes, const float* x_scales, int64_t T, int64_t K,
+                             const muse_int8_weight* w, int64_t N, void* out, int32_t out_dtype, int64_t ldo,
+                             uint32_t* status, void* stream) {
+  MUSE_TRY(validate_int8(T, K, w, N, out, out_dtype, ldo, status));
+  if (T == 0) return MUSE_OK;
+  if (!aligned_to(x_codes, 16) || !aligned_to(x_scales, 4)) return MUSE_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return out_dtype == MUSE_BF16 ? int8_product<__nv_bfloat16>(x_codes, x_scales, T, K, *w, N, out, ldo, status, st)
+                                : int8_product<float>(x_codes, x_scales, T, K, *w, N, out, ldo, status, st);
+}
+
+muse_status muse_int8_linear_workspace_size(int64_t T, int64_t K, size_t* bytes) {
+  if (bytes == nullptr || T < 0 || K < 16 || K % 16 != 0) return MUSE_ERR_INVALID_ARG;
+  if (K > 131072 || T > (int64_t(1) << 24)) return MUSE_ERR_UNSUPPORTED;
+  *bytes = align_up(static_cast<size_t>(T * K), kAlign) + align_up(sizeof(float) * T, kAlign);
+  return MUSE_OK;
+}
+
+muse_status muse_int8_linear(const void* x, int32_t x_dtype, int64_t T, int64_t K, int64_t ldx,
+                             const muse_int8_weight* w, int64_t N, void* out, int32_t out_dtype, int64_t ldo,
+                             void* workspace, size_t workspace_bytes, uint32_t* status, void* stream) {
+  MUSE_TRY(validate_int8(T, K, w, N, out, out_dtype, ldo, status));
+  if (!valid_dtype(x_dtype) || ldx < K) return MUSE_ERR_INVALID_ARG;
+  if (ldx > (int64_t(1) << 40)) return MUSE_ERR_UNSUPPORTED;
+  if (T == 0) return MUSE_OK;
+  if (!aligned_to(x, dtype_size(x_dtype))) return MUSE_ERR_INVALID_ARG;
+  size_t need = 0;
+  MUSE_TRY(muse_int8_linear_workspace_size(T, K, &need));
+  if (!aligned_to(workspace, kAlign) || workspace_bytes < need) return MUSE_ERR_WORKSPACE;
+  float* scales = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align_up(static_cast<size_t>(T * K), kAlign));
+  MUSE_TRY(quantize_int8(x, x_dtype, T, K, ldx, workspace, scales, static_cast<cudaStream_t>(stream)));
+  return muse_int8_matmul(workspace, scales, T, K, w, N, out, out_dtype, ldo, status, stream);
+}
+
+muse_status muse_latent_moe_few_tokens_workspace_size(const muse_moe_config* cfg, size_t* bytes) {
+  if (bytes == nullptr) return MUSE_ERR_INVALID_ARG;
+  MUSE_TRY(validate_few(cfg));
+  *bytes = few_layout(*cfg).total;
+  return MUSE_OK;
+}
+
+muse_status muse_latent_moe_few_tokens(const muse_moe_config* cfg, const void* x, const void* W_router,
+                                       const void* W_pool, const void* W_gate, const void* W_up, const void* W_down,
+                                       const void* gamma, const void* W_unpool, void* out, void* stream) {
+  MUSE_TRY(validate_few(cfg));
+  const void* ptrs[] = {x, W_router, W_pool, gamma, W_unpool, out};
+  for (const void* p : ptrs)
+    if (p == nullptr || !aligned16(p)) return MUSE_ERR_INVALID_ARG;
+  MUSE_TRY(validate_experts(cfg, W_gate, W_up, W_down));
+  MUSE_TRY(validate_options(cfg));
+  if (!aligned_to(cfg->workspace, kAlign) || cfg->workspace_bytes < few_layout(*cfg).total) return MUSE_ERR_WORKSPACE;
+  return few_tokens_impl(*cfg, x, W_router, W_pool, W_gate, W_up, W_down, gamma, W_unpool, out,
+                         static_cast<cudaStream_t>(stream));
+}
+
+muse_status muse_latent_moe_few_tokens_checked(const muse_moe_config* cfg, const muse_tensor* x,
+                                               const muse_tensor* W_router, const muse_tensor* W_pool,
+                                               const muse_tensor* W_gate, const muse_tensor* W_up,
+                                               const muse_tensor* W_down, const muse_tensor* gamma,
+                                               const muse_tensor* W_unpool, const muse_tensor* out, void* stream) {
+  MUSE_TRY(validate_few(cfg));
+  ExpertOperands e;
+  MUSE_TRY(check_tensors(*cfg, x, W_router, W_pool, W_gate, W_up, W_down, gamma, W_unpool, out, &e));
+  return muse_latent_moe_few_tokens(cfg, x->data, W_router->data, W_pool->data, e.gate, e.up, e.down, gamma->data,
+                                    W_unpool->data, const_cast<void*>(out->data), stream);
+}
+
+muse_status muse_latent_moe_few_tokens_status(const muse_moe_config* cfg, void* stream, uint32_t* detail) {
+  MUSE_TRY(validate_few(cfg));
+  if (cfg->workspace == nullptr) return MUSE_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  MUSE_CK(cudaStreamSynchronize(st));
+  uint32_t word[2] = {0, 0};
+  MUSE_CK(cudaMemcpy(word, cfg->workspace, sizeof(word), cudaMemcpyDeviceToHost));
+  if (detail != nullptr) *detail = word[1];
+  return static_cast<muse_status>(word[0]);
 }
 
 muse_status muse_selftest_bounded_wait(uint64_t limit_ns, uint32_t* status_dev, void* stream) {
