@@ -7,6 +7,7 @@ If the compiled library is missing, importing works but every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Dict, Optional
@@ -83,11 +84,7 @@ def tensor_desc(t) -> Tensor:
     is described as it is, and the library rejects it)."""
     import torch
     elem = {torch.float32: ELEM_F32, torch.bfloat16: ELEM_BF16, torch.uint8: ELEM_U8}.get(t.dtype, -1)
-    d = Tensor()
-    d.data, d.elem, d.ndim = int(t.data_ptr()), elem, t.dim()
-    for i in range(min(t.dim(), 3)):
-        d.shape[i], d.stride[i] = int(t.shape[i]), int(t.stride(i))
-    return d
+    return Tensor(t.data_ptr(), elem, t.dim(), tuple(t.shape[:3]), tuple(t.stride()[:3]))
 
 
 class Nvfp4Weight(ctypes.Structure):
@@ -260,20 +257,19 @@ def forward_checked(cfg: Config, x, W_router, W_pool, W_gate, W_up, W_down, gamm
                   W_gate, W_up, W_down, gamma, W_unpool, out, stream)
 
 
+def _weight_descs(W_router, W_pool, W_gate, W_up, W_down, gamma, W_unpool):
+    """The muse_tensor arrays of a layer's weights, in argument order (NVFP4 experts: three each)."""
+    def descs(t):
+        parts = t if isinstance(t, (tuple, list)) else (t,)
+        return (Tensor * len(parts))(*[tensor_desc(p) for p in parts])
+    return tuple(descs(t) for t in (W_router, W_pool, W_gate, W_up, W_down, gamma, W_unpool))
+
+
 def _call_checked(fn, name: str, cfg: Config, x, W_router, W_pool, W_gate, W_up, W_down, gamma, W_unpool, out,
                   stream) -> None:
-    def one(t):
-        return ctypes.byref(tensor_desc(t))
-
-    def expert(t):
-        if isinstance(t, (tuple, list)):
-            arr = (Tensor * 3)(*[tensor_desc(p) for p in t])
-            return ctypes.cast(arr, ctypes.POINTER(Tensor)), arr
-        d = tensor_desc(t)
-        return ctypes.pointer(d), d
-    eg, eu, ed = expert(W_gate), expert(W_up), expert(W_down)
-    code = fn(ctypes.byref(cfg), one(x), one(W_router), one(W_pool), eg[0], eu[0], ed[0], one(gamma), one(W_unpool),
-              one(out), _stream_handle(stream))
+    weights = _weight_descs(W_router, W_pool, W_gate, W_up, W_down, gamma, W_unpool)
+    code = fn(ctypes.byref(cfg), ctypes.byref(tensor_desc(x)), *weights, ctypes.byref(tensor_desc(out)),
+              _stream_handle(stream))
     _check(code, name)
 
 
@@ -417,7 +413,7 @@ def _one_device(*tensors):
     dev = tensors[0].device
     if dev.type != "cuda" or any(t.device != dev for t in tensors):
         raise ValueError("tensors must be on one CUDA device")
-    return torch.cuda.device(dev)
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
 def quantize_int8_rows(src, codes=None, scales=None, stream=None):
@@ -586,6 +582,11 @@ class LatentMoE:
         except MuseError as e:
             if e.code != 2:  # MUSE_ERR_UNSUPPORTED
                 raise
+        # its configuration and the weights' descriptors, once: a call of a few microseconds would
+        # otherwise spend more time on marshalling than on the GPU
+        self._few_config = self.config(min(T_max, FEW_TOKENS), self.few_workspace)
+        self._few_weights = _weight_descs(weights["W_router"], weights["W_pool"], *self.experts, weights["gamma"],
+                                          weights["W_unpool"])
 
     def config(self, T: int, workspace=None) -> Config:
         return block_config(T, self.dims, self.dtype, self.modes, self.w, self.nvfp4, workspace)
@@ -617,11 +618,13 @@ class LatentMoE:
         for t, dtype in ((topk_idx, torch.int32), (topk_w, torch.float32)):
             if t is not None and (t.shape != (T, self.dims["k"]) or t.dtype != dtype or t.device != x.device):
                 raise ValueError(f"topk_idx and topk_w are [{T}, {self.dims['k']}] int32 and float32 on x's device")
-        w = self.w
-        with _one_device(x, w["W_router"]):
-            cfg = self.config(T, self.few_workspace)
-            cfg.topk_idx_out, cfg.topk_w_out = _ptr(topk_idx), _ptr(topk_w)
+        with _one_device(x, self.w["W_router"]):
+            cfg = Config.from_buffer_copy(self._few_config)
+            cfg.T, cfg.topk_idx_out, cfg.topk_w_out = T, _ptr(topk_idx), _ptr(topk_w)
             if out is None:
                 out = torch.empty((T, self.dims["D"]), dtype=x.dtype, device=x.device)
-            few_tokens(cfg, x, w["W_router"], w["W_pool"], *self.experts, w["gamma"], w["W_unpool"], out, stream)
+            code = lib().muse_latent_moe_few_tokens_checked(
+                ctypes.byref(cfg), ctypes.byref(tensor_desc(x)), *self._few_weights, ctypes.byref(tensor_desc(out)),
+                _stream_handle(stream))
+            _check(code, "muse_latent_moe_few_tokens_checked")
         return out

@@ -1,20 +1,41 @@
 // few_tokens.cuh -- the whole latent-MoE layer for at most 8 tokens in one kernel.
 //
 // With a few tokens the layer is a chain of matrix-vector products whose weights are read
-// once: W_router and W_pool, the selected experts' W_gate / W_up, their W_down, W_unpool.
-// One cooperative launch (one CTA per SM, all resident) runs the chain in phases separated
-// by grid barriers:
+// once: W_router and W_pool, the selected experts' W_gate / W_up, their W_down, W_unpool. It
+// is bound by reading them, and by the latency of the steps between. One cooperative launch
+// (one CTA per SM, all resident) runs the chain in phases separated by grid barriers:
 //   0  xn = rmsnorm(x)                                    (only with ffn_pre_gain)
 //   1  l = W_router xn, z = W_pool xn
 //   1b z = rmsnorm(z)                                     (only with pre_norm_gain)
-//   2  every CTA: top-k of l, the list of distinct experts and their tokens
-//      h = silu(W_gate[e] z) * (W_up[e] z)
+//      every CTA: top-k of l, the list of distinct experts and their tokens
+//   2  h = silu(W_gate[e] z) * (W_up[e] z)
 //   3  y = W_down[e] h, per-CTA partial sums of squares of y (times its gain, input-scaled)
 //   4  c = sum_j g_j y_j / rms_j (1 + gamma)
 //   5  out = W_unpool c
 //   6  post norm and residual gate                        (only with those)
 // y and the sublayer's f stay FP32; z, h and c are stored in the type the next product
 // reads (bf16; f16 for NVFP4 experts, whose decoded weights are f16; float32).
+//
+// Work split: the weight rows of a phase (of all distinct experts in a row) are divided evenly
+// over the CTAs by row, whatever the tile, so no SM waits for another's larger share; a row is
+// always summed whole, by the same warps in the same order, so its result does not depend on
+// the split.
+//
+// Roles (4 producer warps, 16 consumer warps). Three producer warps stream a CTA's weight rows
+// through a ring of stages, up to 32 rows x kc elements each, by 16-byte asynchronous copies
+// (any row count and row start; the row distance in shared memory is padded so that the
+// fragment reads below are free of bank conflicts); the fourth adds the n <= 8 activation rows
+// of the same K range. At a phase's start the ring fills with the new phase's weights while
+// the grid barrier is still pending -- only the activations wait for it -- so DRAM stays busy
+// through the barriers, except for the one before phase 2, whose rows the routing decides.
+// (One bulk copy per row piece, from one producer warp, instead: one token through the full-size
+// bf16 layer in 331 us, against 171.)
+// The consumer warps split each stage along K. 16-bit weights go to the warp-level MMA (m16n8k16:
+// weight rows as A, the tokens as its 8 columns): lane (g, t) of a warp reads 16 consecutive
+// bytes of rows g and g + 8 and of token g, and the MMA's K order is that of these bytes in both
+// operands. NVFP4 rows are decoded in registers into the A fragment (gemv_fp4.cuh). float32 rows are
+// multiplied in FP32, a lane per row, the activations broadcast. After a chunk of rows the
+// warps' partial sums are added in warp order through shared memory.
 #pragma once
 
 #include <cstdint>
@@ -32,9 +53,42 @@ namespace muse {
 constexpr int kFewTokens = 8;         // most tokens of one call
 constexpr int kFewAssign = 8 * 32;    // most (token, expert) pairs: top_k <= 32
 constexpr int kFewGridMax = 256;      // CTAs a workspace has partial sums for
-constexpr int kFewThreads = 512;
+constexpr int kFewWarps = 16;         // consumer warps
+constexpr int kFewProducers = 4;      // producer warps: one for activations, the others for weights
+constexpr int kFewThreads = 32 * (kFewProducers + kFewWarps);
+constexpr int kFewConsumers = 32 * kFewWarps;
+constexpr int kFewRows = 32;          // weight rows of a stage (gate/up: 16 features of each)
+constexpr int kFewMaxStages = 16;
+constexpr int kFewBarriers = 7;       // grid barriers of a call, their counters 128 bytes apart
+constexpr uint32_t kFewRedBytes = kFewWarps * 8u * 33u * 4u;  // partial sums of a chunk
+
+enum FewFormat : int { FEW_BF16 = 0, FEW_NVFP4 = 1, FEW_F32 = 2 };
+
+// How the stages of a product with weights of a format lie in shared memory: kc elements of K
+// per stage, so that every consumer warp has a share of each (its unit: 32 bf16 elements, 64
+// NVFP4, 4 float32); weight rows wstride bytes apart from offset 0, NVFP4 block scales sstride
+// apart from soff, activation rows xstride apart from xoff. The row distances keep the
+// consumers' reads free of bank conflicts: bf16 rows 64 bytes past a multiple of 128 (a quarter
+// warp reads 64 bytes of two rows), float rows 16 past it (eight lanes read one row each), codes
+// 32 (half a warp reads 32 bytes of four rows), scales an odd multiple of 16, f16 activations
+// beside codes 16 (32 bytes a lane, in two reads).
+template <int FORMAT>
+struct FewGeo {
+  static constexpr int kc = FORMAT == FEW_NVFP4 ? 1024 : FORMAT == FEW_BF16 ? 512 : 256;
+  static constexpr uint32_t row_bytes = FORMAT == FEW_NVFP4 ? kc / 2 : FORMAT == FEW_BF16 ? kc * 2 : kc * 4;
+  static constexpr uint32_t act_bytes = FORMAT == FEW_F32 ? kc * 4 : kc * 2;
+  static constexpr uint32_t wstride = row_bytes + (FORMAT == FEW_NVFP4 ? 32 : FORMAT == FEW_BF16 ? 64 : 16);
+  static constexpr uint32_t soff = kFewRows * wstride;
+  static constexpr uint32_t sstride = FORMAT == FEW_NVFP4 ? (kc / 16) | 16 : 0;
+  static constexpr uint32_t xoff = soff + kFewRows * sstride;
+  static constexpr uint32_t xstride = act_bytes + (FORMAT == FEW_BF16 ? 64 : 16);
+  // bytes of a stage with n activation rows
+  static constexpr uint32_t bytes(int n) { return xoff + static_cast<uint32_t>(n) * xstride; }
+};
 
 struct FewArgs {
+  int stages;             // ring depth
+  uint32_t stage_bytes;
   int T, D, L, I, E, k;
   int router_mode, norm_mode, gamma_shared;
   float eps, logit_scale, rsf, pre_norm_eps, ffn_pre_eps, ffn_post_eps, inv_temp, gate_eps;
@@ -53,37 +107,31 @@ struct FewArgs {
   void *xn, *z, *h, *c;
 };
 
-// Grid barrier number i (0, 1, ...) of one launch: every CTA adds one to the counter (zeroed
-// before the launch) and waits until all have. All CTAs are resident (cooperative launch), so
-// the wait ends; it is bounded all the same: past the limit the status word records a timeout
-// and the CTA leaves. Returns the same value on every thread of the CTA.
+// Grid barriers: every CTA adds one to the barrier's counter (zeroed before the launch) when
+// its part is done, and waits, when it needs the others', until all have. All CTAs are resident
+// (cooperative launch), so the wait ends; it is bounded all the same. Once a wait of a CTA has
+// run out, *abort is set, the status word holds the timeout, and the CTA goes through the rest
+// of the call without waiting or copying, so that every thread leaves.
 __device__ __forceinline__ uint32_t ld_acquire_u32(const uint32_t* p) {
   uint32_t v;
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ bool few_wait_counter(const uint32_t* counter, uint32_t target, uint32_t* status,
-                                                 uint32_t detail) {
-  if (ld_acquire_u32(counter) >= target) return true;
+__device__ __forceinline__ void red_release_u32(uint32_t* p, uint32_t v) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ void few_poll(const uint32_t* counter, uint32_t target, volatile int* abort,
+                                         uint32_t* status, uint32_t detail) {
+  if (ld_acquire_u32(counter) >= target) return;
   const uint64_t t0 = globaltimer_ns();
   while (ld_acquire_u32(counter) < target) {
+    if (*abort) return;
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      *abort = 1;
       record_status(status, kStatusTimeout, detail);
-      return false;
+      return;
     }
   }
-  return true;
-}
-__device__ __forceinline__ bool few_grid_barrier(uint32_t* counter, int i, uint32_t* status, int* flag) {
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    atomicAdd(counter, 1u);
-    *flag = few_wait_counter(counter, static_cast<uint32_t>(i + 1) * gridDim.x, status, 0xF00u + i) ? 1 : 0;
-    __threadfence();
-  }
-  __syncthreads();
-  return *flag != 0;
 }
 
 // ---------------------------------------------------------------------- routing
@@ -220,256 +268,597 @@ __device__ __forceinline__ void few_lists(const FewArgs& p, FewRoute& r, int tid
   sync();
 }
 
-// ---------------------------------------------------------------------- products
+// ---------------------------------------------------------------------- the row streams
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 // (saturating: a latent beyond f16's range does not become an infinity, as in the gather of
 // the token-tiled forward)
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return f32_to_f16_sat(v); }
 
-// One weight row against n <= 8 activation rows by a warp: lanes stride over K, eight
-// elements at a time, FP32 sums, a butterfly at the end (every lane gets the sums).
-template <typename TW, typename TX>
-__device__ __forceinline__ void few_row_dot(const TW* w, const TX* const* x, int n, int K, int lane, float (&acc)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
-  for (int k0 = lane * 8; k0 < K; k0 += 256) {
-    float wv[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) wv[i] = to_f32(w[k0 + i]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[j] = fmaf(wv[i], to_f32(x[j][k0 + i]), acc[j]);
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) acc[j] = warp_sum(acc[j]);
+__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The same for an NVFP4 row: codes [K / 2] and block scales [K / 16] (matrix scale left out).
-__device__ __forceinline__ void few_row_dot_fp4(const uint8_t* codes, const uint8_t* scales, const __half* const* x,
-                                                int n, int K, int lane, float (&acc)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
-  for (int k0 = lane * 8; k0 < K; k0 += 256) {
-    uint32_t q[4];
-    e2m1x8_to_f16x2(*reinterpret_cast<const uint32_t*>(codes + k0 / 2), q[0], q[1], q[2], q[3]);
-    const uint32_t s = e4m3_bcast_f16x2(scales[k0 / 16], 0);
-    float wv[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t v = f16x2_mul(q[i], s);
-      const __half2 h = *reinterpret_cast<const __half2*>(&v);
-      wv[2 * i] = __low2float(h);
-      wv[2 * i + 1] = __high2float(h);
+enum FewPhase : int { FEW_IN = 0, FEW_GATE_UP = 1, FEW_DOWN = 2, FEW_OUT = 3 };
+
+// A CTA's rows of a phase in order: units [u0, u1) of U (unit: a weight row; gate/up: a feature),
+// `group` units per expert (dense: all of them), cut into chunks of at most `most` units of one
+// expert, the chunks of an expert's share as equal as possible.
+struct FewChunks {
+  int u, u1, group, most;
+  int d, f, len;  // current chunk: expert number, first unit within it, units
+  __device__ __forceinline__ FewChunks(int64_t U, int group_, int most_) : group(group_), most(most_) {
+    u = static_cast<int>(U * blockIdx.x / gridDim.x);
+    u1 = static_cast<int>(U * (blockIdx.x + 1) / gridDim.x);
+    take();
+  }
+  __device__ __forceinline__ bool done() const { return u >= u1; }
+  __device__ __forceinline__ void take() {
+    d = u / group;
+    f = u - d * group;
+    const int left = min(u1 - u, group - f);
+    const int n = (left + most - 1) / most;
+    len = n > 0 ? (left + n - 1) / n : 0;
+  }
+  __device__ __forceinline__ void next() {
+    u += len;
+    take();
+  }
+};
+
+// the CTA whose share of U units holds unit u
+__device__ __forceinline__ int few_owner(int64_t U, int64_t u) {
+  return static_cast<int>(((u + 1) * gridDim.x - 1) / U);
+}
+
+struct FewRing {
+  uint32_t bar0, base;  // full barriers, then empty ones; first stage
+  int stages, stage;
+  uint32_t phase, stage_bytes;
+  __device__ __forceinline__ uint32_t full() const { return bar0 + 8u * stage; }
+  __device__ __forceinline__ uint32_t empty() const { return bar0 + 8u * (kFewMaxStages + stage); }
+  __device__ __forceinline__ uint32_t addr() const { return base + stage_bytes * stage; }
+  __device__ __forceinline__ void next() {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1u;
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[j] = fmaf(wv[i], __half2float(x[j][k0 + i]), acc[j]);
   }
+};
+
+template <typename TA, bool FP4>
+struct FewTypes {
+  using Z = typename std::conditional<FP4, __half, TA>::type;  // z and h
+};
+
+// ---- producers --------------------------------------------------------------------------
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// one arrival on bar once this thread's copies so far have landed (counted in the barrier's
+// expected arrivals)
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// The product a phase computes, as its producers see it: a chunk's weight rows, which follow one
+// another in one or two matrices, and its activation rows.
+template <typename TA, bool FP4, int PHASE>
+struct FewSource {
+  using TZ = typename FewTypes<TA, FP4>::Z;
+  static constexpr bool kExperts = PHASE == FEW_GATE_UP || PHASE == FEW_DOWN;
+  static constexpr int kFormat = FP4 && kExperts ? FEW_NVFP4 : sizeof(TA) == 2 ? FEW_BF16 : FEW_F32;
+  const FewArgs& p;
+  const FewRoute& r;
+  const TA* xin;
+  int K;
+
+  __device__ __forceinline__ int64_t row_bytes() const {
+    return kFormat == FEW_NVFP4 ? K / 2 : K * static_cast<int64_t>(sizeof(TA));
+  }
+  // index of the chunk's first row over all experts
+  __device__ __forceinline__ int64_t first_row(const FewChunks& c) const {
+    return c.f + (kExperts ? static_cast<int64_t>(r.ids[c.d]) * (PHASE == FEW_DOWN ? p.L : p.I) : 0);
+  }
+  // row i of the chunk, i < 32 (gate/up: 0.. gate, 16.. up)
+  __device__ __forceinline__ const uint8_t* row(const FewChunks& c, int i) const {
+    const void* w;
+    int64_t at = first_row(c) + i;
+    if constexpr (PHASE == FEW_IN) {
+      w = at < p.E ? p.W_router : p.W_pool;
+      at = at < p.E ? at : at - p.E;
+    } else if constexpr (PHASE == FEW_OUT) {
+      w = p.W_unpool;
+    } else if constexpr (PHASE == FEW_GATE_UP) {
+      w = i < 16 ? p.W_gate : p.W_up;
+      at -= i < 16 ? 0 : 16;
+    } else {
+      w = p.W_down;
+    }
+    return static_cast<const uint8_t*>(w) + at * row_bytes();
+  }
+  __device__ __forceinline__ const uint8_t* scales(const FewChunks& c, int i) const {
+    const uint8_t* s = PHASE == FEW_DOWN ? p.s_down : i < 16 ? p.s_gate : p.s_up;
+    return s + (first_row(c) + (PHASE == FEW_DOWN ? i : i & 15)) * (K / 16);
+  }
+  __device__ __forceinline__ bool has_row(const FewChunks& c, int i) const {
+    return (PHASE == FEW_GATE_UP ? (i & 15) : i) < c.len;
+  }
+  __device__ __forceinline__ int tokens(const FewChunks& c) const {
+    return kExperts ? r.first[c.d + 1] - r.first[c.d] : p.T;
+  }
+  __device__ __forceinline__ const uint8_t* activation(const FewChunks& c, int j) const {
+    const void* x;
+    if constexpr (PHASE == FEW_IN) {
+      x = xin + static_cast<int64_t>(j) * K;
+    } else if constexpr (PHASE == FEW_GATE_UP) {
+      x = static_cast<const TZ*>(p.z) + static_cast<int64_t>(r.pair[r.first[c.d] + j] / p.k) * K;
+    } else if constexpr (PHASE == FEW_DOWN) {
+      x = static_cast<const TZ*>(p.h) + static_cast<int64_t>(r.first[c.d] + j) * K;
+    } else {
+      x = static_cast<const TA*>(p.c) + static_cast<int64_t>(j) * K;
+    }
+    return static_cast<const uint8_t*>(x);
+  }
+};
+
+// One producer warp's copies of a phase: warp 0 the activations (and NVFP4 block scales), once
+// `ready` (the barrier before this phase; nullptr: nothing to wait for) has passed; the others
+// each every third weight row, as far ahead as the ring is free. A stage's addresses advance by
+// constants from those of the chunk, so that a copy costs a few instructions.
+template <typename TA, bool FP4, int PHASE>
+__device__ __forceinline__ void few_produce(const FewSource<TA, FP4, PHASE>& q, FewChunks c, FewRing& ring,
+                                            const uint32_t* ready, volatile int* abort, int pw, int lane) {
+  constexpr int kFormat = FewSource<TA, FP4, PHASE>::kFormat;
+  using G = FewGeo<kFormat>;
+  constexpr int kWeightWarps = kFewProducers - 1;
+  constexpr int kMine = (kFewRows + kWeightWarps - 1) / kWeightWarps;
+  const FewArgs& p = q.p;
+  const int K = q.K;
+  if (pw == 0 && ready != nullptr) {
+    if (lane == 0) few_poll(ready, gridDim.x, abort, p.status, 0xB00u + PHASE);
+    __syncwarp();
+  }
+  for (; !c.done(); c.next()) {
+    if (pw == 0) {
+      const int n = q.tokens(c);
+      const uint8_t* x = q.activation(c, min(lane, n - 1));  // lane j: token j's row
+      // block scales: four 16-byte pieces of a row's 64 bytes a stage, a row per four lanes
+      const uint8_t* sc[4];
+      if constexpr (kFormat == FEW_NVFP4) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) acc[j] = warp_sum(acc[j]);
+        for (int a = 0; a < 4; ++a) sc[a] = q.scales(c, min(8 * a + (lane >> 2), kFewRows - 1)) + 16 * (lane & 3);
+      }
+      for (int k0 = 0; k0 < K; k0 += G::kc) {
+        const int kn = min(G::kc, K - k0);
+        // (a wait that gave up: no copies; the arrivals go on so that nobody waits for them)
+        const bool ok = mbar_wait(ring.empty(), ring.phase ^ 1u, abort, p.status, 0xA00u + ring.stage);
+        if (__all_sync(0xffffffffu, ok)) {
+          const uint32_t st = ring.addr();
+          const int bytes = kn * static_cast<int>(G::act_bytes / G::kc);
+          for (int j = 0; j < n; ++j) {
+            const uint8_t* xj = reinterpret_cast<const uint8_t*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x), j));
+#pragma unroll
+            for (int o = 16 * lane; o < static_cast<int>(G::act_bytes); o += 512)
+              if (o < bytes) cp_async16(st + G::xoff + G::xstride * j + o, xj + o);
+          }
+          if constexpr (kFormat == FEW_NVFP4) {
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+              const int i = 8 * a + (lane >> 2);
+              if (q.has_row(c, i) && 16 * (lane & 3) < kn / 16)
+                cp_async16(st + G::soff + G::sstride * i + 16 * (lane & 3), sc[a]);
+            }
+          }
+        }
+        cp_async_arrive(ring.full());
+        ring.next();
+        x += G::act_bytes;
+        if constexpr (kFormat == FEW_NVFP4) {
+#pragma unroll
+          for (int a = 0; a < 4; ++a) sc[a] += G::kc / 16;
+        }
+      }
+    } else {
+      // rows i = pw - 1 + kWeightWarps * m; two runs of consecutive rows: before and after `cut`
+      // (router / pooler; gate / up), whose distances are the matrix' row bytes
+      const int cut = PHASE == FEW_GATE_UP ? 16 : PHASE == FEW_IN ? max(0, min(kFewRows, p.E - c.f)) : kFewRows;
+      const int64_t step = q.row_bytes();
+      const uint8_t* w0 = q.row(c, 0) + 16 * lane;
+      const uint8_t* w1 = cut < kFewRows ? q.row(c, cut) - cut * step + 16 * lane : w0;
+      uint32_t mask = 0;
+#pragma unroll
+      for (int m = 0; m < kMine; ++m) {
+        const int i = pw - 1 + kWeightWarps * m;
+        if (i < kFewRows && q.has_row(c, i)) mask |= 1u << m;
+      }
+      for (int k0 = 0; k0 < K; k0 += G::kc) {
+        const int bytes = min(G::kc, K - k0) * static_cast<int>(G::row_bytes) / G::kc;
+        const bool ok = mbar_wait(ring.empty(), ring.phase ^ 1u, abort, p.status, 0xA00u + ring.stage);
+        if (__all_sync(0xffffffffu, ok)) {
+          const uint32_t st = ring.addr() + 16 * lane + G::wstride * (pw - 1);
+          const uint8_t* a0 = w0 + (pw - 1) * step;
+          const uint8_t* a1 = w1 + (pw - 1) * step;
+#pragma unroll
+          for (int m = 0; m < kMine; ++m) {
+            const uint8_t* a = pw - 1 + kWeightWarps * m < cut ? a0 : a1;
+            if (mask & (1u << m)) {
+#pragma unroll
+              for (int o = 0; o < static_cast<int>(G::row_bytes); o += 512)
+                if (o + 16 * lane < bytes) cp_async16(st + kWeightWarps * m * G::wstride + o, a + o);
+            }
+            a0 += kWeightWarps * step;
+            a1 += kWeightWarps * step;
+          }
+        }
+        cp_async_arrive(ring.full());
+        ring.next();
+        w0 += G::row_bytes;
+        w1 += G::row_bytes;
+      }
+    }
+  }
 }
 
-// Centred RMSNorm of one row by the whole CTA: dst = src / sqrt(mean(src^2) + eps) * (1 + w).
-template <typename TS, typename TG, typename TD>
-__device__ __forceinline__ void few_norm_row(const TS* src, const TG* w, TD* dst, int n, float eps, float* part) {
-  float s = 0.0f;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const float v = to_f32(src[i]);
-    s = fmaf(v, v, s);
+// ---- consumers --------------------------------------------------------------------------
+__device__ __forceinline__ void few_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kFewConsumers) : "memory"); }
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float4 as_float4(uint4 v) {
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+
+// One chunk's products: the stages of 32 weight rows and n activation rows, this warp's share
+// of K; afterwards red[warp][token][row] (rows 33 floats apart) holds the warp's sums.
+template <int FORMAT>
+__device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int K, int n, int wc, int lane,
+                                            volatile int* abort, float* red) {
+  using G = FewGeo<FORMAT>;
+  const int g = lane >> 2, t = lane & 3;
+  const int gx = min(g, n - 1);  // token rows past n are not staged (their columns are not used)
+  float acc[8];  // MMA: two 16-row tiles of 4; float32: this lane's row, 8 tokens
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+  float(&lo)[4] = *reinterpret_cast<float(*)[4]>(&acc[0]);
+  float(&hi)[4] = *reinterpret_cast<float(*)[4]>(&acc[4]);
+  for (int k0 = 0; k0 < K; k0 += G::kc) {
+    const int kn = min(G::kc, K - k0);
+    mbar_wait(ring.full(), ring.phase, abort, p.status, 0xC00u + ring.stage);
+    __syncwarp();
+    const uint32_t st = ring.addr();
+    if constexpr (FORMAT == FEW_BF16) {
+      const uint32_t w = st + g * G::wstride + t * 16u, x = st + G::xoff + gx * G::xstride + t * 16u;
+      const uint32_t r8 = 8u * G::wstride;
+#pragma unroll 2
+      for (int s = wc; s < kn / 32; s += kFewWarps) {  // 32 elements = 64 bytes of each row
+        const uint32_t o = 64u * s;
+        const uint4 b = lds128(x + o), a0 = lds128(w + o), a1 = lds128(w + r8 + o), a2 = lds128(w + 2 * r8 + o),
+                    a3 = lds128(w + 3 * r8 + o);
+        mma_bf16_16816(lo, a0.x, a1.x, a0.y, a1.y, b.x, b.y);
+        mma_bf16_16816(hi, a2.x, a3.x, a2.y, a3.y, b.x, b.y);
+        mma_bf16_16816(lo, a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+        mma_bf16_16816(hi, a2.z, a3.z, a2.w, a3.w, b.z, b.w);
+      }
+    } else if constexpr (FORMAT == FEW_NVFP4) {
+      const uint32_t w = st + g * G::wstride + t * 8u, x = st + G::xoff + gx * G::xstride + t * 32u;
+      const uint32_t sc = st + G::soff + g * G::sstride;
+      for (int s = wc; s < kn / 64; s += kFewWarps) {  // 64 elements; this lane's 16-weight block: t
+        const uint4 x0 = lds128(x + 128u * s), x1 = lds128(x + 128u * s + 16u);
+        const uint32_t xv[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          uint32_t a[2][8];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t rr = 16u * m + 8u * i;
+            const uint2 c = lds64(w + rr * G::wstride + 32u * s);
+            const uint32_t b = e4m3_bcast_f16x2(lds32(sc + rr * G::sstride + 4u * s), static_cast<uint32_t>(t));
+            e2m1x8_to_f16x2(c.x, a[i][0], a[i][1], a[i][2], a[i][3]);
+            e2m1x8_to_f16x2(c.y, a[i][4], a[i][5], a[i][6], a[i][7]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) a[i][q] = f16x2_mul(a[i][q], b);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            mma_f16_16816(m == 0 ? lo : hi, a[0][2 * q], a[1][2 * q], a[0][2 * q + 1], a[1][2 * q + 1], xv[2 * q],
+                          xv[2 * q + 1]);
+        }
+      }
+    } else {
+      const uint32_t w = st + lane * G::wstride, x = st + G::xoff;
+#pragma unroll 2
+      for (int s = wc; s < kn / 4; s += kFewWarps) {
+        const float4 a = as_float4(lds128(w + 16u * s));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j >= n) break;
+          const float4 b = as_float4(lds128(x + j * G::xstride + 16u * s));
+          acc[j] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, acc[j]))));
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(ring.empty());
+    ring.next();
   }
-  const float scale = 1.0f / sqrtf(block_sum(s, part) / static_cast<float>(n) + eps);
-  for (int i = threadIdx.x; i < n; i += blockDim.x) dst[i] = from_f32<TD>(to_f32(src[i]) * scale * (1.0f + to_f32(w[i])));
+  float* mine = red + wc * 8 * 33;
+  if constexpr (FORMAT == FEW_F32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mine[j * 33 + lane] = acc[j];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mine[(2 * t + (i & 1)) * 33 + 16 * (i >> 2) + 8 * ((i >> 1) & 1) + g] = acc[i];
+  }
+}
+
+// The warps' sums of (token, row), in warp order.
+__device__ __forceinline__ float few_sum(const float* red, int token, int row) {
+  float v = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kFewWarps; ++w) v += red[(w * 8 + token) * 33 + row];
+  return v;
 }
 
 __device__ __forceinline__ float few_silu(float a) { return a / (1.0f + expf(-a)); }
 
+// Sum over the consumer threads, the same on each (part: 32 floats).
+__device__ __forceinline__ float few_block_sum(float v, float* part, int wc, int lane) {
+  v = warp_sum(v);
+  few_sync();
+  if (lane == 0) part[wc] = v;
+  few_sync();
+  return warp_sum(lane < kFewWarps ? part[lane] : 0.0f);
+}
+
+// Centred RMSNorm of one row by the consumers: dst = src / sqrt(mean(src^2) + eps) * (1 + w).
+template <typename TS, typename TG, typename TD>
+__device__ __forceinline__ void few_norm_row(const TS* src, const TG* w, TD* dst, int n, float eps, float* part,
+                                             int tid) {
+  float s = 0.0f;
+  for (int i = tid; i < n; i += kFewConsumers) {
+    const float v = to_f32(src[i]);
+    s = fmaf(v, v, s);
+  }
+  const float scale = 1.0f / sqrtf(few_block_sum(s, part, tid >> 5, tid & 31) / static_cast<float>(n) + eps);
+  for (int i = tid; i < n; i += kFewConsumers) dst[i] = from_f32<TD>(to_f32(src[i]) * scale * (1.0f + to_f32(w[i])));
+}
+
 // TA: activations, dense weights, gains and the output (bf16 or float). FP4: NVFP4 experts
 // (TA = bf16; z and h are f16).
 template <typename TA, bool FP4>
-__global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const FewArgs p) {
-  using TZ = typename std::conditional<FP4, __half, TA>::type;
+__global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_constant__ FewArgs p) {
+  using TZ = typename FewTypes<TA, FP4>::Z;
+  constexpr int DENSE = sizeof(TA) == 4 ? FEW_F32 : FEW_BF16;
+  constexpr int EXPERT = FP4 ? FEW_NVFP4 : DENSE;
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ FewRoute route;
+  __shared__ __align__(8) uint64_t bars[2 * kFewMaxStages];
   __shared__ float part[32];
-  __shared__ int flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-  const int gw = blockIdx.x * nw + warp, ngw = gridDim.x * nw;
+  __shared__ float scale_s[kFewAssign];
+  __shared__ int abort_flag;
+  volatile int* abort = &abort_flag;
+  float* red = reinterpret_cast<float*>(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int T = p.T, D = p.D, L = p.L, I = p.I, E = p.E, k = p.k;
-  int bar = 0;
-  const TA* xin = static_cast<const TA*>(p.x);
-  if (p.ffn_pre_gain != nullptr) {
-    TA* xn = static_cast<TA*>(p.xn);
-    for (int t = blockIdx.x; t < T; t += gridDim.x)
-      few_norm_row(xin + static_cast<int64_t>(t) * D, static_cast<const TA*>(p.ffn_pre_gain),
-                   xn + static_cast<int64_t>(t) * D, D, p.ffn_pre_eps, part);
-    xin = xn;
-    if (!few_grid_barrier(p.barrier, bar++, p.status, &flag)) return;
-  }
-  // phase 1
-  {
-    const TA* xr[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) xr[j] = xin + static_cast<int64_t>(j < T ? j : 0) * D;
-    for (int r = gw; r < E + L; r += ngw) {
-      const TA* w = r < E ? static_cast<const TA*>(p.W_router) + static_cast<int64_t>(r) * D
-                          : static_cast<const TA*>(p.W_pool) + static_cast<int64_t>(r - E) * D;
-      float acc[8];
-      few_row_dot(w, xr, T, D, lane, acc);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < T && lane == j) {
-          if (r < E) p.logits[static_cast<int64_t>(j) * E + r] = acc[j];
-          else static_cast<TZ*>(p.z)[static_cast<int64_t>(j) * L + r - E] = from_f32<TZ>(acc[j]);
-        }
+  FewRing ring{smem_u32(bars), smem_u32(smem) + kFewRedBytes, p.stages, 0, 0u, p.stage_bytes};
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(smem_u32(bars + s), 32 * kFewProducers);
+      mbar_init(smem_u32(bars + kFewMaxStages + s), kFewWarps);
     }
+    abort_flag = 0;
+    fence_mbar_init();
   }
-  if (!few_grid_barrier(p.barrier, bar++, p.status, &flag)) return;
+  __syncthreads();
+  auto counter = [&](int i) { return p.barrier + 32 * i; };
+  const TA* xin = p.ffn_pre_gain != nullptr ? static_cast<const TA*>(p.xn) : static_cast<const TA*>(p.x);
+  auto route_ready = [] { asm volatile("bar.sync 2, %0;" ::"n"(kFewThreads) : "memory"); };
+
+  if (warp < kFewProducers) {
+    few_produce(FewSource<TA, FP4, FEW_IN>{p, route, xin, D}, FewChunks(E + L, E + L, kFewRows), ring,
+                p.ffn_pre_gain != nullptr ? counter(0) : nullptr, abort, warp, lane);
+    route_ready();
+    const int nd = route.distinct;
+    few_produce(FewSource<TA, FP4, FEW_GATE_UP>{p, route, xin, L},
+                FewChunks(static_cast<int64_t>(nd) * I, I, kFewRows / 2), ring,
+                counter(p.pre_norm_gain != nullptr ? 2 : 1), abort, warp, lane);
+    few_produce(FewSource<TA, FP4, FEW_DOWN>{p, route, xin, I}, FewChunks(static_cast<int64_t>(nd) * L, L, kFewRows),
+                ring, counter(3), abort, warp, lane);
+    few_produce(FewSource<TA, FP4, FEW_OUT>{p, route, xin, L}, FewChunks(D, D, kFewRows), ring, counter(5),
+                abort, warp, lane);
+    cp_async_wait_all();  // nothing in flight when the CTA leaves, also after a wait that gave up
+    return;
+  }
+
+  const int wc = warp - kFewProducers, tid = threadIdx.x - 32 * kFewProducers;
+  // this CTA's part of barrier i is done: its global writes are visible to whoever sees the count
+  auto arrive = [&](int i) {
+    __threadfence();
+    few_sync();
+    if (tid == 0) red_release_u32(counter(i), 1u);
+  };
+  auto wait = [&](int i) {
+    if (tid == 0) few_poll(counter(i), gridDim.x, abort, p.status, 0xF00u + i);
+    few_sync();
+  };
+  // one phase's chunks; store(chunk, token, lane's row, sum) runs on warp `token` of the consumers
+  auto products = [&](auto format, FewChunks c, int K, bool by_expert, auto store) {
+    for (; !c.done(); c.next()) {
+      const int n = by_expert ? route.first[c.d + 1] - route.first[c.d] : T;
+      few_consume<decltype(format)::value>(p, ring, K, n, wc, lane, abort, red);
+      few_sync();
+      for (int j = wc; j < n; j += kFewWarps) store(c, j, few_sum(red, j, lane));
+      few_sync();
+    }
+  };
+  using Dense = std::integral_constant<int, DENSE>;
+  using Expert = std::integral_constant<int, EXPERT>;
+
+  if (p.ffn_pre_gain != nullptr) {
+    for (int t = blockIdx.x; t < T; t += gridDim.x)
+      few_norm_row(static_cast<const TA*>(p.x) + static_cast<int64_t>(t) * D, static_cast<const TA*>(p.ffn_pre_gain),
+                   static_cast<TA*>(p.xn) + static_cast<int64_t>(t) * D, D, p.ffn_pre_eps, part, tid);
+    arrive(0);
+  }
+  products(Dense{}, FewChunks(E + L, E + L, kFewRows), D, false, [&](const FewChunks& c, int j, float v) {
+    const int r = c.f + lane;
+    if (lane < c.len) {
+      if (r < E) p.logits[static_cast<int64_t>(j) * E + r] = v;
+      else static_cast<TZ*>(p.z)[static_cast<int64_t>(j) * L + r - E] = from_f32<TZ>(v);
+    }
+  });
+  arrive(1);
+  wait(1);
   if (p.pre_norm_gain != nullptr) {
     TZ* z = static_cast<TZ*>(p.z);
     for (int t = blockIdx.x; t < T; t += gridDim.x)
       few_norm_row(z + static_cast<int64_t>(t) * L, static_cast<const TA*>(p.pre_norm_gain),
-                   z + static_cast<int64_t>(t) * L, L, p.pre_norm_eps, part);
-    if (!few_grid_barrier(p.barrier, bar++, p.status, &flag)) return;
+                   z + static_cast<int64_t>(t) * L, L, p.pre_norm_eps, part, tid);
+    arrive(2);
   }
-  few_route(p, route, warp, nw, lane);
-  __syncthreads();
-  few_lists(p, route, threadIdx.x, blockDim.x, [] { __syncthreads(); });
+  few_route(p, route, wc, kFewWarps, lane);
+  few_sync();
+  few_lists(p, route, tid, kFewConsumers, [] { few_sync(); });
+  route_ready();
   const int nd = route.distinct;
-  // phase 2
+  products(Expert{}, FewChunks(static_cast<int64_t>(nd) * I, I, kFewRows / 2), L, true,
+           [&](const FewChunks& c, int j, float v) {
+             const float u = __shfl_down_sync(0xffffffffu, v, 16);
+             float mg = 1.0f, mu = 1.0f;
+             if constexpr (FP4) {
+               mg = p.m_gate[route.ids[c.d]];
+               mu = p.m_up[route.ids[c.d]];
+             }
+             if (lane < c.len)
+               static_cast<TZ*>(p.h)[static_cast<int64_t>(route.first[c.d] + j) * I + c.f + lane] =
+                   from_f32<TZ>(few_silu(v * mg) * (u * mu));
+           });
+  arrive(3);
   {
-    const TZ* z = static_cast<const TZ*>(p.z);
-    for (int r = gw; r < nd * I; r += ngw) {
-      const int d = r / I, f = r - d * I, e = route.ids[d];
-      const int64_t row = static_cast<int64_t>(e) * I + f;
-      for (int p0 = route.first[d]; p0 < route.first[d + 1]; p0 += 8) {
-        const int n = min(8, route.first[d + 1] - p0);
-        const TZ* xr[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) xr[j] = z + static_cast<int64_t>(route.pair[p0 + (j < n ? j : 0)] / k) * L;
-        float g[8], u[8];
-        float mg = 1.0f, mu = 1.0f;
-        if constexpr (FP4) {
-          few_row_dot_fp4(static_cast<const uint8_t*>(p.W_gate) + row * (L / 2), p.s_gate + row * (L / 16), xr, n, L, lane, g);
-          few_row_dot_fp4(static_cast<const uint8_t*>(p.W_up) + row * (L / 2), p.s_up + row * (L / 16), xr, n, L, lane, u);
-          mg = p.m_gate[e];
-          mu = p.m_up[e];
-        } else {
-          few_row_dot(static_cast<const TA*>(p.W_gate) + row * L, xr, n, L, lane, g);
-          few_row_dot(static_cast<const TA*>(p.W_up) + row * L, xr, n, L, lane, u);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < n && lane == j)
-            static_cast<TZ*>(p.h)[static_cast<int64_t>(p0 + j) * I + f] = from_f32<TZ>(few_silu(g[j] * mg) * (u[j] * mu));
-      }
-    }
-  }
-  if (!few_grid_barrier(p.barrier, bar++, p.status, &flag)) return;
-  // phase 3
-  {
-    const TZ* h = static_cast<const TZ*>(p.h);
-    for (int r = gw; r < nd * L; r += ngw) {
-      const int d = r / L, f = r - d * L, e = route.ids[d];
-      const int64_t row = static_cast<int64_t>(e) * L + f;
-      for (int p0 = route.first[d]; p0 < route.first[d + 1]; p0 += 8) {
-        const int n = min(8, route.first[d + 1] - p0);
-        const TZ* xr[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) xr[j] = h + static_cast<int64_t>(p0 + (j < n ? j : 0)) * I;
-        float y[8];
-        float ms = 1.0f;
-        if constexpr (FP4) {
-          few_row_dot_fp4(static_cast<const uint8_t*>(p.W_down) + row * (I / 2), p.s_down + row * (I / 16), xr, n, I, lane, y);
-          ms = p.m_down[e];
-        } else {
-          few_row_dot(static_cast<const TA*>(p.W_down) + row * I, xr, n, I, lane, y);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < n && lane == j) p.y[static_cast<int64_t>(p0 + j) * L + f] = y[j] * ms;
-      }
-    }
-  }
-  if (!few_grid_barrier(p.barrier, bar++, p.status, &flag)) return;
-  // phase 4: token by token; every position's mean square by one warp
-  {
-    TA* c = static_cast<TA*>(p.c);
+    // sums of squares of the rows this CTA computed of each position (lane 0 of the token's warp)
+    float ss = 0.0f;
+    int ss_d = -1;
+    auto flush = [&](int j) {
+      if (ss_d >= 0 && lane == 0) p.ss[static_cast<int64_t>(route.first[ss_d] + j) * kFewGridMax + blockIdx.x] = ss;
+    };
     const TA* gamma = static_cast<const TA*>(p.gamma);
-    __shared__ float scale_s[32];
-    for (int t = blockIdx.x; t < T; t += gridDim.x) {
-      for (int j = warp; j < k; j += nw) {
-        const int a = t * k + j;
-        const float* y = p.y + static_cast<int64_t>(route.pos[a]) * L;
-        const TA* gm = gamma + (p.gamma_shared ? 0 : static_cast<int64_t>(route.expert[a]) * L);
-        float s = 0.0f;
-        for (int i = lane; i < L; i += 32) {
-          const float u = __ldcg(y + i) * (p.norm_mode == 1 ? 1.0f + to_f32(gm[i]) : 1.0f);
-          s = fmaf(u, u, s);
-        }
-        s = warp_sum(s);
-        if (lane == 0) scale_s[j] = route.weight[a] / sqrtf(s / static_cast<float>(L) + p.eps);
+    const int64_t dn = static_cast<int64_t>(nd) * L;
+    FewChunks c(dn, L, kFewRows);
+    int last_n = 0;
+    for (; !c.done(); c.next()) {
+      const int n = route.first[c.d + 1] - route.first[c.d], e = route.ids[c.d];
+      few_consume<EXPERT>(p, ring, I, n, wc, lane, abort, red);
+      few_sync();
+      if (c.d != ss_d) {
+        if (wc < last_n) flush(wc);
+        ss = 0.0f;
+        ss_d = c.d;
+        last_n = n;
       }
-      __syncthreads();
-      for (int i = threadIdx.x; i < L; i += blockDim.x) {
-        float acc = 0.0f;
-        for (int j = 0; j < k; ++j) {
-          const int a = t * k + j;
-          const float gm = to_f32(gamma[(p.gamma_shared ? 0 : static_cast<int64_t>(route.expert[a]) * L) + i]);
-          acc = fmaf(scale_s[j] * (1.0f + gm), __ldcg(p.y + static_cast<int64_t>(route.pos[a]) * L + i), acc);
+      if (wc < n) {
+        float y = few_sum(red, wc, lane);
+        if constexpr (FP4) y *= p.m_down[e];
+        float u = 0.0f;
+        if (lane < c.len) {
+          p.y[static_cast<int64_t>(route.first[c.d] + wc) * L + c.f + lane] = y;
+          u = y;
+          if (p.norm_mode == 1)
+            u *= 1.0f + to_f32(gamma[(p.gamma_shared ? 0 : static_cast<int64_t>(e) * L) + c.f + lane]);
         }
-        c[static_cast<int64_t>(t) * L + i] = from_f32<TA>(acc);
+        ss += warp_sum(u * u);
       }
-      __syncthreads();
+      few_sync();
     }
-  }
-  if (!few_grid_barrier(p.barrier, bar++, p.status, &flag)) return;
-  // phase 5
-  const bool finish = p.ffn_post_gain != nullptr || p.residual_gate != nullptr;
-  {
-    const TA* xr[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) xr[j] = static_cast<const TA*>(p.c) + static_cast<int64_t>(j < T ? j : 0) * L;
-    for (int r = gw; r < D; r += ngw) {
-      float acc[8];
-      few_row_dot(static_cast<const TA*>(p.W_unpool) + static_cast<int64_t>(r) * L, xr, T, L, lane, acc);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < T && lane == j) {
-          if (finish) p.f[static_cast<int64_t>(j) * D + r] = acc[j];
-          else static_cast<TA*>(p.out)[static_cast<int64_t>(j) * D + r] = from_f32<TA>(acc[j]);
-        }
-    }
-  }
-  if (!finish) return;
-  if (!few_grid_barrier(p.barrier, bar++, p.status, &flag)) return;
-  // phase 6
-  for (int t = blockIdx.x; t < T; t += gridDim.x) {
-    const float* f = p.f + static_cast<int64_t>(t) * D;
-    const TA* w = static_cast<const TA*>(p.ffn_post_gain);
-    float scale = 1.0f;
-    if (w != nullptr) {
+    if (wc < last_n) flush(wc);
+    arrive(4);
+    wait(4);
+    // phase 4: every pair's weight over its root mean square, from the CTAs that hold its rows
+    for (int a = wc; a < T * k; a += kFewWarps) {
+      const int pos = route.pos[a];
+      int d = 0;
+      for (int i = lane; i < nd; i += 32)
+        if (route.first[i] <= pos) d = i;
+      d = __reduce_max_sync(0xffffffffu, d);
+      const int c0 = few_owner(dn, static_cast<int64_t>(d) * L), c1 = few_owner(dn, static_cast<int64_t>(d + 1) * L - 1);
       float s = 0.0f;
-      for (int i = threadIdx.x; i < D; i += blockDim.x) {
-        const float v = __ldcg(f + i) * (1.0f + to_f32(w[i]));
-        s = fmaf(v, v, s);
-      }
-      scale = 1.0f / sqrtf(block_sum(s, part) / static_cast<float>(D) + p.ffn_post_eps);
+      for (int i = c0 + lane; i <= c1; i += 32)  // (with fewer rows than CTAs, some have none)
+        if (dn * i / gridDim.x < dn * (i + 1) / gridDim.x) s += __ldcg(p.ss + static_cast<int64_t>(pos) * kFewGridMax + i);
+      s = warp_sum(s);
+      if (lane == 0) scale_s[a] = route.weight[a] / sqrtf(s / static_cast<float>(L) + p.eps);
     }
-    for (int i = threadIdx.x; i < D; i += blockDim.x) {
-      float v = __ldcg(f + i);
-      if (w != nullptr) v *= (1.0f + to_f32(w[i])) * scale;
-      if (p.residual_gate != nullptr) {
-        const float wg = p.residual_gate[i] * p.inv_temp;
-        const float beta = 1.0f / (1.0f + expf(-wg));
-        const float alpha = sqrtf(fmaxf((1.0f / (1.0f + expf(wg))) * (1.0f + beta), p.gate_eps));
-        v = alpha * to_f32(static_cast<const TA*>(p.x)[static_cast<int64_t>(t) * D + i]) + beta * v;
+    few_sync();
+    for (int i = blockIdx.x * kFewConsumers + tid; i < T * L; i += gridDim.x * kFewConsumers) {
+      const int t = i / L, f = i - t * L;
+      float acc = 0.0f;
+#pragma unroll 8
+      for (int j = 0; j < k; ++j) {
+        const int a = t * k + j;
+        const float gm = to_f32(gamma[(p.gamma_shared ? 0 : static_cast<int64_t>(route.expert[a]) * L) + f]);
+        acc = fmaf(scale_s[a] * (1.0f + gm), __ldcg(p.y + static_cast<int64_t>(route.pos[a]) * L + f), acc);
       }
-      static_cast<TA*>(p.out)[static_cast<int64_t>(t) * D + i] = from_f32<TA>(v);
+      static_cast<TA*>(p.c)[i] = from_f32<TA>(acc);
     }
+    arrive(5);
+  }
+  const bool finish = p.ffn_post_gain != nullptr || p.residual_gate != nullptr;
+  const TA* post = static_cast<const TA*>(p.ffn_post_gain);
+  float ssf = 0.0f;  // of this CTA's rows of token wc
+  products(Dense{}, FewChunks(D, D, kFewRows), L, false, [&](const FewChunks& c, int j, float v) {
+    const int64_t o = static_cast<int64_t>(j) * D + c.f + lane;
+    if (!finish) {
+      if (lane < c.len) static_cast<TA*>(p.out)[o] = from_f32<TA>(v);
+      return;
+    }
+    float u = 0.0f;
+    if (lane < c.len) {
+      p.f[o] = v;
+      if (post != nullptr) u = v * (1.0f + to_f32(post[c.f + lane]));
+    }
+    ssf += warp_sum(u * u);
+  });
+  if (!finish) return;
+  if (wc < T && lane == 0) p.ssf[wc * kFewGridMax + blockIdx.x] = ssf;
+  arrive(6);
+  wait(6);
+  // phase 6
+  for (int t = wc; t < T; t += kFewWarps) {
+    float s = 0.0f;
+    for (int i = lane; i < static_cast<int>(gridDim.x); i += 32) s += __ldcg(p.ssf + t * kFewGridMax + i);
+    s = warp_sum(s);
+    if (lane == 0) scale_s[t] = 1.0f / sqrtf(s / static_cast<float>(D) + p.ffn_post_eps);
+  }
+  few_sync();
+  for (int i = blockIdx.x * kFewConsumers + tid; i < T * D; i += gridDim.x * kFewConsumers) {
+    const int t = i / D, f = i - t * D;
+    float v = __ldcg(p.f + i);
+    if (post != nullptr) v *= (1.0f + to_f32(post[f])) * scale_s[t];
+    if (p.residual_gate != nullptr) {
+      const float wg = p.residual_gate[f] * p.inv_temp;
+      const float beta = 1.0f / (1.0f + expf(-wg));
+      const float alpha = sqrtf(fmaxf((1.0f / (1.0f + expf(wg))) * (1.0f + beta), p.gate_eps));
+      v = alpha * to_f32(static_cast<const TA*>(p.x)[i]) + beta * v;
+    }
+    static_cast<TA*>(p.out)[i] = from_f32<TA>(v);
   }
 }
 

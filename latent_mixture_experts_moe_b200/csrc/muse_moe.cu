@@ -1130,8 +1130,9 @@ muse_status check_tensors(const muse_moe_config& c, const muse_tensor* x, const 
 }
 
 // ---------------------------------------------------------------------- a few tokens
-// Workspace of muse_latent_moe_few_tokens: status word and barrier counter (one 256-byte
-// block, zeroed by every call), then the intermediates.
+// Workspace of muse_latent_moe_few_tokens: status word and barrier counters (zeroed by every
+// call), then the intermediates.
+constexpr size_t kFewHeader = 128 * (1 + kFewBarriers);
 struct FewLayout {
   size_t logits, xn, z, h, y, ss, c, f, ssf, total;
 };
@@ -1147,7 +1148,7 @@ FewLayout few_layout(const muse_moe_config& c) {
   FewLayout l{};
   const size_t as = act_size(c), T = c.T, A = c.T * c.top_k;
   const bool finish = c.ffn_post_gain != nullptr || c.residual_gate != nullptr;
-  size_t o = kAlign;
+  size_t o = align_up(kFewHeader, kAlign);
   auto take = [&](size_t bytes) {
     const size_t at = o;
     o = align_up(o + bytes, kAlign);
@@ -1170,9 +1171,16 @@ template <typename TA, bool FP4>
 muse_status launch_few(FewArgs& a, cudaStream_t st) {
   auto kern = k_few_tokens<TA, FP4>;
   const int grid = std::min(sm_count(), kFewGridMax);
+  constexpr uint32_t kSmem = 227 * 1024 - 12 * 1024;  // less the static shared memory
+  constexpr int kDense = sizeof(TA) == 2 ? FEW_BF16 : FEW_F32;
+  a.stage_bytes = static_cast<uint32_t>(
+      align_up(std::max(FewGeo<kDense>::bytes(a.T), FewGeo<FP4 ? FEW_NVFP4 : kDense>::bytes(a.T)), 128));
+  a.stages = static_cast<int>(std::min<uint32_t>(kFewMaxStages, (kSmem - kFewRedBytes) / a.stage_bytes));
+  const size_t smem = kFewRedBytes + static_cast<size_t>(a.stages) * a.stage_bytes;
   void* args[] = {&a};
-  MUSE_CK(cudaMemsetAsync(a.status, 0, kAlign, st));
-  MUSE_CK(cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kern), dim3(grid), dim3(kFewThreads), args, 0, st));
+  MUSE_CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+  MUSE_CK(cudaMemsetAsync(a.status, 0, kFewHeader, st));
+  MUSE_CK(cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kern), dim3(grid), dim3(kFewThreads), args, smem, st));
   return MUSE_OK;
 }
 
