@@ -5,9 +5,8 @@
 // is bound by reading them, and by the latency of the steps between. One cooperative launch
 // (one CTA per SM, all resident) runs the chain in phases separated by grid barriers:
 //   0  xn = rmsnorm(x)                                    (only with ffn_pre_gain)
-//   1  l = W_router xn, z = W_pool xn
-//   1b z = rmsnorm(z)                                     (only with pre_norm_gain)
-//      every CTA: top-k of l, the list of distinct experts and their tokens
+//   1  l = W_router xn; then z = W_pool xn, while every CTA finds the top-k of l and lists the
+//      distinct experts and their tokens; z = rmsnorm(z) (only with pre_norm_gain)
 //   2  h = silu(W_gate[e] z) * (W_up[e] z)
 //   3  y = W_down[e] h, per-CTA partial sums of squares of y (times its gain, input-scaled)
 //   4  c = sum_j g_j y_j / rms_j (1 + gamma)
@@ -21,21 +20,23 @@
 // always summed whole, by the same warps in the same order, so its result does not depend on
 // the split.
 //
-// Roles (4 producer warps, 16 consumer warps). Three producer warps stream a CTA's weight rows
-// through a ring of stages, up to 32 rows x kc elements each, by 16-byte asynchronous copies
-// (any row count and row start; the row distance in shared memory is padded so that the
-// fragment reads below are free of bank conflicts); the fourth adds the n <= 8 activation rows
-// of the same K range. At a phase's start the ring fills with the new phase's weights while
-// the grid barrier is still pending -- only the activations wait for it -- so DRAM stays busy
-// through the barriers, except for the one before phase 2, whose rows the routing decides.
-// (One bulk copy per row piece, from one producer warp, instead: one token through the full-size
-// bf16 layer in 331 us, against 171.)
-// The consumer warps split each stage along K. 16-bit weights go to the warp-level MMA (m16n8k16:
+// Roles (24 warps). Producers (4): three stream a CTA's weight rows through a ring of stages, up
+// to 32 rows x kc elements each, by 16-byte asynchronous copies (any row count and row start;
+// the row distance in shared memory is padded so that the fragment reads below are free of
+// bank conflicts); the fourth adds the n <= 8 activation rows of the same K range. At a phase's
+// start the ring fills with the new phase's weights while the grid barrier is still pending
+// -- only the activations wait for it -- so DRAM stays busy through the barriers. (One bulk
+// copy per row piece, from one producer warp, instead: one token through the full-size bf16
+// layer in 331 us, against 171 with these copies.)
+// Products (16): they split each stage along K. 16-bit weights go to the warp-level MMA (m16n8k16:
 // weight rows as A, the tokens as its 8 columns): lane (g, t) of a warp reads 16 consecutive
 // bytes of rows g and g + 8 and of token g, and the MMA's K order is that of these bytes in both
-// operands. NVFP4 rows are decoded in registers into the A fragment (gemv_fp4.cuh). float32 rows are
-// multiplied in FP32, a lane per row, the activations broadcast. After a chunk of rows the
-// warps' partial sums are added in warp order through shared memory.
+// operands. NVFP4 rows are decoded in registers into the A fragment (gemv_fp4.cuh). float32 rows
+// are multiplied in FP32, a lane per row, the activations broadcast. The warps' partial sums of a
+// chunk of rows go to one of two buffers.
+// Store (4): they add the partial sums in a fixed order, apply what follows the product and
+// write the result, while the product warps go on with the next chunk. The router's rows come
+// first, so that two store warps select the experts while the pooler's rows stream.
 #pragma once
 
 #include <cstdint>
@@ -52,15 +53,16 @@ namespace muse {
 
 constexpr int kFewTokens = 8;         // most tokens of one call
 constexpr int kFewAssign = 8 * 32;    // most (token, expert) pairs: top_k <= 32
-constexpr int kFewGridMax = 256;      // CTAs a workspace has partial sums for
-constexpr int kFewWarps = 16;         // consumer warps
+constexpr int kFewGridMax = 192;      // CTAs a workspace has partial sums for
 constexpr int kFewProducers = 4;      // producer warps: one for activations, the others for weights
-constexpr int kFewThreads = 32 * (kFewProducers + kFewWarps);
-constexpr int kFewConsumers = 32 * kFewWarps;
+constexpr int kFewStore = 4;          // store warps
+constexpr int kFewWarps = 16;         // product warps
+constexpr int kFewThreads = 32 * (kFewProducers + kFewStore + kFewWarps);
 constexpr int kFewRows = 32;          // weight rows of a stage (gate/up: 16 features of each)
 constexpr int kFewMaxStages = 16;
-constexpr int kFewBarriers = 7;       // grid barriers of a call, their counters 128 bytes apart
-constexpr uint32_t kFewRedBytes = kFewWarps * 8u * 33u * 4u;  // partial sums of a chunk
+constexpr int kFewBarriers = 8;       // grid barriers of a call, their counters 128 bytes apart
+constexpr uint32_t kFewRedFloats = kFewWarps * 8u * 33u;      // partial sums of a chunk
+constexpr uint32_t kFewRedBytes = 2u * kFewRedFloats * 4u;    // two chunks'
 
 enum FewFormat : int { FEW_BF16 = 0, FEW_NVFP4 = 1, FEW_F32 = 2 };
 
@@ -143,49 +145,65 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 }
 
 // The k largest keys of a token by one warp, in descending order, ties to the lower expert:
-// lane j < k receives the j-th. NPL keys per lane (E <= 32 NPL). Each round is one warp-wide
-// maximum and one minimum over the lanes that hold it; only the lane that owned the winner
-// looks for its next best.
+// lane j < k receives the j-th and its logit. NPL keys per lane (E <= 32 NPL). Each round is
+// one warp-wide maximum and one minimum over the lanes that hold it; only the lane that owned
+// the winner looks for its next best.
 template <int NPL>
 __device__ __forceinline__ int few_topk(const float* l, const float* bias, int mode, float scale, int E, int k,
-                                        int lane) {
+                                        int lane, float& logit) {
+  constexpr bool kKeep = NPL <= 8;  // the logits stay in registers (more would spill)
   uint32_t key[NPL];
+  float val[kKeep ? NPL : 1];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      const int e = lane + 32 * i;
+      val[i] = e < E ? __ldcg(l + e) : 0.0f;
+    }
+  }
+  uint32_t best = 0;
+  int bi = 0;
+  float bv = 0.0f;
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
     const int e = lane + 32 * i;
     key[i] = 0;  // below every real key (-inf has 0x007fffff)
     if (e < E) {
-      const float li = __ldcg(l + e);
+      const float li = kKeep ? val[kKeep ? i : 0] : __ldcg(l + e);
       float kv = (mode == 0) ? li : 1.0f / (1.0f + expf(-scale * li));
       if (bias != nullptr) kv += bias[e];
       key[i] = order_key(kv);
     }
   }
-  uint32_t best = 0;
-  int bi = 0;
   auto rescan = [&]() {
     best = 0;
-    bi = 0;
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
       if (key[i] > best) {
         best = key[i];
         bi = i;
+        if (kKeep) bv = val[kKeep ? i : 0];
       }
   };
   rescan();
   int mine = 0;
+#pragma unroll 1
   for (int j = 0; j < k; ++j) {
     const uint32_t top = __reduce_max_sync(0xffffffffu, best);
     const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? static_cast<uint32_t>(lane + 32 * bi) : 0xffffffffu);
-    if (best == top && static_cast<uint32_t>(lane + 32 * bi) == e) {
+    const float v = __shfl_sync(0xffffffffu, bv, static_cast<int>(e & 31));
+    if (lane == j) {
+      mine = static_cast<int>(e);
+      logit = v;
+    }
+    if (lane == static_cast<int>(e & 31)) {
 #pragma unroll
       for (int i = 0; i < NPL; ++i)
         if (i == bi) key[i] = 0;
       rescan();
     }
-    if (lane == j) mine = static_cast<int>(e);
   }
+  if (!kKeep && lane < k) logit = __ldcg(l + mine);
   return mine;
 }
 
@@ -193,79 +211,84 @@ __device__ __forceinline__ int few_topk(const float* l, const float* bias, int m
 // (token, slot) pairs by expert, then by pair; the pairs of distinct expert d are the
 // positions first[d] .. first[d + 1] - 1.
 struct FewRoute {
-  int expert[kFewAssign];      // [t * k + j]
+  __align__(16) int expert[kFewAssign];  // [t * k + j]; past the last pair: INT_MAX
   float weight[kFewAssign];
-  int pos[kFewAssign];         // pair -> position
-  int pair[kFewAssign];        // position -> pair
-  int rank[kFewAssign];        // pair -> number of its expert among the distinct ones
-  int ids[kFewAssign];         // distinct expert -> expert
+  int pos[kFewAssign];                   // pair -> position
+  int token[kFewAssign];                 // position -> token
+  int ids[kFewAssign];                   // distinct expert -> expert
   int first[kFewAssign + 1];
+  uint32_t seen[32];                     // bit e % 32 of word e / 32: expert e is selected
   int distinct;
 };
 
-__device__ __forceinline__ void few_route(const FewArgs& p, FewRoute& r, int warp, int nwarps, int lane) {
-  for (int t = warp; t < p.T; t += nwarps) {
-    const float* l = p.logits + static_cast<int64_t>(t) * p.E;
-    int sel;
-    if (p.E <= 64) sel = few_topk<2>(l, p.router_bias, p.router_mode, p.logit_scale, p.E, p.k, lane);
-    else if (p.E <= 256) sel = few_topk<8>(l, p.router_bias, p.router_mode, p.logit_scale, p.E, p.k, lane);
-    else sel = few_topk<32>(l, p.router_bias, p.router_mode, p.logit_scale, p.E, p.k, lane);
-    const bool mine = lane < p.k;
-    const float lj = mine ? __ldcg(l + sel) : 0.0f;
-    float g;
-    if (p.router_mode == 0) {
-      const float m = warp_max(mine ? lj : neg_inf());
-      const float pj = mine ? expf(lj - m) : 0.0f;
-      g = pj / warp_sum(pj);
-    } else {
-      const float sj = mine ? 1.0f / (1.0f + expf(-p.logit_scale * lj)) : 0.0f;
-      g = p.rsf * sj / (warp_sum(sj) + 1e-15f);
-    }
-    if (mine) {
-      const int a = t * p.k + lane;
-      r.expert[a] = sel;
-      r.weight[a] = g;
-      if (blockIdx.x == 0) {
-        if (p.idx_out != nullptr) p.idx_out[a] = sel;
-        if (p.w_out != nullptr) p.w_out[a] = g;
-      }
+// Token t's experts and weights, by one warp.
+__device__ __forceinline__ void few_route(const FewArgs& p, FewRoute& r, int t, int lane) {
+  const float* l = p.logits + static_cast<int64_t>(t) * p.E;
+  int sel;
+  float lj = 0.0f;
+  if (p.E <= 64) sel = few_topk<2>(l, p.router_bias, p.router_mode, p.logit_scale, p.E, p.k, lane, lj);
+  else if (p.E <= 256) sel = few_topk<8>(l, p.router_bias, p.router_mode, p.logit_scale, p.E, p.k, lane, lj);
+  else sel = few_topk<32>(l, p.router_bias, p.router_mode, p.logit_scale, p.E, p.k, lane, lj);
+  const bool mine = lane < p.k;
+  float g;
+  if (p.router_mode == 0) {
+    const float m = warp_max(mine ? lj : neg_inf());
+    const float pj = mine ? expf(lj - m) : 0.0f;
+    g = pj / warp_sum(pj);
+  } else {
+    const float sj = mine ? 1.0f / (1.0f + expf(-p.logit_scale * lj)) : 0.0f;
+    g = p.rsf * sj / (warp_sum(sj) + 1e-15f);
+  }
+  if (mine) {
+    const int a = t * p.k + lane;
+    r.expert[a] = sel;
+    r.weight[a] = g;
+    atomicOr(&r.seen[sel >> 5], 1u << (sel & 31));
+    if (blockIdx.x == 0) {
+      if (p.idx_out != nullptr) p.idx_out[a] = sel;
+      if (p.w_out != nullptr) p.w_out[a] = g;
     }
   }
 }
 
-// positions, distinct experts: every thread of a group of nthreads calls it with a barrier
-// over the group between the two steps (sync)
-template <typename Sync>
-__device__ __forceinline__ void few_lists(const FewArgs& p, FewRoute& r, int tid, int nthreads, Sync sync) {
-  const int A = p.T * p.k;
-  for (int a = tid; a < A; a += nthreads) {
+// Positions and distinct experts, from expert[] and seen[], by a group of nthreads (all of
+// whose warps call it; a barrier over the group before and after).
+__device__ __forceinline__ void few_lists(const FewArgs& p, FewRoute& r, int tid, int nthreads) {
+  const int A = p.T * p.k, lane = tid & 31;
+  // distinct experts below word `lane` of seen
+  const uint32_t word = r.seen[lane];
+  int below = __popc(word);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, below, o);
+    if (lane >= o) below += u;
+  }
+  if (tid == 31) {
+    r.distinct = below;
+    r.first[below] = A;
+  }
+  below -= __popc(word);
+  for (int a0 = tid & ~31; a0 < A; a0 += nthreads) {
+    const int a = a0 + lane;
     const int e = r.expert[a];
-    int pos = 0, same = 0;
-    for (int b = 0; b < A; ++b) {
-      const int eb = r.expert[b];
-      pos += (eb < e) || (eb == e && b < a);
-      same += (eb == e && b < a);
+    int less = 0, same = 0;
+#pragma unroll 2
+    for (int b = 0; b < A; b += 4) {
+      const int4 v = *reinterpret_cast<const int4*>(&r.expert[b]);
+      less += (v.x < e) + (v.y < e) + (v.z < e) + (v.w < e);
+      same += (v.x == e && b < a) + (v.y == e && b + 1 < a) + (v.z == e && b + 2 < a) + (v.w == e && b + 3 < a);
     }
-    r.pos[a] = pos;
-    r.pair[pos] = a;
-    r.rank[a] = same;  // 0: the first pair of its expert
+    const int es = min(e, 1023);
+    const int d = __shfl_sync(0xffffffffu, below, es >> 5) + __popc(__shfl_sync(0xffffffffu, word, es >> 5) & ((1u << (es & 31)) - 1u));
+    if (a < A) {
+      r.pos[a] = less + same;
+      r.token[less + same] = a / p.k;
+      if (same == 0) {
+        r.ids[d] = e;
+        r.first[d] = less;
+      }
+    }
   }
-  sync();
-  for (int a = tid; a < A; a += nthreads) {
-    if (r.rank[a] != 0) continue;
-    const int e = r.expert[a];
-    int d = 0;
-    for (int b = 0; b < A; ++b) d += (r.rank[b] == 0 && r.expert[b] < e);
-    r.ids[d] = e;
-    r.first[d] = r.pos[a];
-  }
-  if (tid == 0) {
-    int n = 0;
-    for (int b = 0; b < A; ++b) n += (r.rank[b] == 0);
-    r.distinct = n;
-    r.first[n] = A;
-  }
-  sync();
 }
 
 // ---------------------------------------------------------------------- the row streams
@@ -283,37 +306,51 @@ __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint3
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-enum FewPhase : int { FEW_IN = 0, FEW_GATE_UP = 1, FEW_DOWN = 2, FEW_OUT = 3 };
+enum FewPhase : int { FEW_ROUTER = 0, FEW_POOL = 1, FEW_GATE_UP = 2, FEW_DOWN = 3, FEW_OUT = 4 };
 
-// A CTA's rows of a phase in order: units [u0, u1) of U (unit: a weight row; gate/up: a feature),
+// A CTA's rows of a phase in order: units [u, u1) of U (unit: a weight row; gate/up: a feature),
 // `group` units per expert (dense: all of them), cut into chunks of at most `most` units of one
-// expert, the chunks of an expert's share as equal as possible.
+// expert, the chunks of an expert's share as equal as possible. CTA c's share starts at
+// floor(U c / G).
+__device__ __forceinline__ int few_share(int U, int c) {
+  const int G = static_cast<int>(gridDim.x), q = U / G;
+  return q * c + (U - q * G) * c / G;
+}
+// the CTA whose share of U units holds unit u (U <= 2^24)
+__device__ __forceinline__ int few_owner(int U, int u) {
+  return static_cast<int>(((static_cast<uint32_t>(u) + 1u) * gridDim.x - 1u) / static_cast<uint32_t>(U));
+}
 struct FewChunks {
-  int u, u1, group, most;
-  int d, f, len;  // current chunk: expert number, first unit within it, units
-  __device__ __forceinline__ FewChunks(int64_t U, int group_, int most_) : group(group_), most(most_) {
-    u = static_cast<int>(U * blockIdx.x / gridDim.x);
-    u1 = static_cast<int>(U * (blockIdx.x + 1) / gridDim.x);
-    take();
+  int left, group, most;   // units left in the share; units per expert, per chunk
+  int d, f, len;           // current chunk: expert number, first unit within it, units
+  int base, extra;         // chunks of the current expert's share: `extra` of base + 1, then of base
+  __device__ __forceinline__ FewChunks(int U, int group_, int most_) : group(group_), most(most_) {
+    const int u0 = few_share(U, blockIdx.x);
+    left = few_share(U, blockIdx.x + 1) - u0;
+    d = u0 / group;
+    f = u0 - d * group;
+    begin();
   }
-  __device__ __forceinline__ bool done() const { return u >= u1; }
-  __device__ __forceinline__ void take() {
-    d = u / group;
-    f = u - d * group;
-    const int left = min(u1 - u, group - f);
-    const int n = (left + most - 1) / most;
-    len = n > 0 ? (left + n - 1) / n : 0;
+  __device__ __forceinline__ bool done() const { return left <= 0; }
+  __device__ __forceinline__ void begin() {
+    const int here = min(left, group - f);
+    const int n = (here + most - 1) / most;
+    base = n > 1 ? here / n : here;
+    extra = here - n * base;
+    len = base + (extra > 0 ? 1 : 0);
   }
   __device__ __forceinline__ void next() {
-    u += len;
-    take();
+    left -= len;
+    f += len;
+    if (f == group) {
+      ++d;
+      f = 0;
+      begin();
+    } else {
+      len = base + (--extra > 0 ? 1 : 0);
+    }
   }
 };
-
-// the CTA whose share of U units holds unit u
-__device__ __forceinline__ int few_owner(int64_t U, int64_t u) {
-  return static_cast<int>(((u + 1) * gridDim.x - 1) / U);
-}
 
 struct FewRing {
   uint32_t bar0, base;  // full barriers, then empty ones; first stage
@@ -336,8 +373,12 @@ struct FewTypes {
 };
 
 // ---- producers --------------------------------------------------------------------------
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// (predicated, not branched around: a producer warp issues many in a row)
+__device__ __forceinline__ void cp_async16_if(bool on, uint32_t dst, const void* src) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(
+                   dst),
+               "l"(src), "r"(static_cast<uint32_t>(on))
+               : "memory");
 }
 // one arrival on bar once this thread's copies so far have landed (counted in the barrier's
 // expected arrivals)
@@ -346,82 +387,73 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// The product a phase computes, as its producers see it: a chunk's weight rows, which follow one
-// another in one or two matrices, and its activation rows.
-template <typename TA, bool FP4, int PHASE>
+// A phase's product: its depth, and its weight rows as units (see FewChunks).
+struct FewJob {
+  int phase, K, U, group, most;
+};
+__device__ __forceinline__ FewJob few_job(const FewArgs& p, int phase, int distinct) {
+  const int rows = phase == FEW_ROUTER ? p.E : phase == FEW_OUT ? p.D : phase == FEW_GATE_UP ? p.I : p.L;
+  const bool experts = phase == FEW_GATE_UP || phase == FEW_DOWN;
+  return {phase, phase <= FEW_POOL ? p.D : phase == FEW_DOWN ? p.I : p.L, experts ? distinct * rows : rows, rows,
+          phase == FEW_GATE_UP ? kFewRows / 2 : kFewRows};
+}
+
+// A job as its producers see it: a chunk's weight rows, which follow one another in one or two
+// matrices, and its activation rows.
+template <typename TA, int FORMAT>
 struct FewSource {
-  using TZ = typename FewTypes<TA, FP4>::Z;
-  static constexpr bool kExperts = PHASE == FEW_GATE_UP || PHASE == FEW_DOWN;
-  static constexpr int kFormat = FP4 && kExperts ? FEW_NVFP4 : sizeof(TA) == 2 ? FEW_BF16 : FEW_F32;
   const FewArgs& p;
   const FewRoute& r;
   const TA* xin;
-  int K;
+  FewJob job;
 
+  __device__ __forceinline__ bool gate_up() const { return job.phase == FEW_GATE_UP; }
+  __device__ __forceinline__ bool experts() const { return job.phase == FEW_GATE_UP || job.phase == FEW_DOWN; }
   __device__ __forceinline__ int64_t row_bytes() const {
-    return kFormat == FEW_NVFP4 ? K / 2 : K * static_cast<int64_t>(sizeof(TA));
+    return FORMAT == FEW_NVFP4 ? job.K / 2 : job.K * static_cast<int64_t>(sizeof(TA));
   }
   // index of the chunk's first row over all experts
   __device__ __forceinline__ int64_t first_row(const FewChunks& c) const {
-    return c.f + (kExperts ? static_cast<int64_t>(r.ids[c.d]) * (PHASE == FEW_DOWN ? p.L : p.I) : 0);
+    return c.f + (experts() ? static_cast<int64_t>(r.ids[c.d]) * job.group : 0);
   }
-  // row i of the chunk, i < 32 (gate/up: 0.. gate, 16.. up)
-  __device__ __forceinline__ const uint8_t* row(const FewChunks& c, int i) const {
-    const void* w;
-    int64_t at = first_row(c) + i;
-    if constexpr (PHASE == FEW_IN) {
-      w = at < p.E ? p.W_router : p.W_pool;
-      at = at < p.E ? at : at - p.E;
-    } else if constexpr (PHASE == FEW_OUT) {
-      w = p.W_unpool;
-    } else if constexpr (PHASE == FEW_GATE_UP) {
-      w = i < 16 ? p.W_gate : p.W_up;
-      at -= i < 16 ? 0 : 16;
-    } else {
-      w = p.W_down;
-    }
-    return static_cast<const uint8_t*>(w) + at * row_bytes();
+  // the chunk's first row in the phase's matrix; gate/up: of W_up if `up`
+  __device__ __forceinline__ const uint8_t* row(const FewChunks& c, bool up) const {
+    const void* w = job.phase == FEW_ROUTER ? p.W_router : job.phase == FEW_POOL ? p.W_pool
+                  : job.phase == FEW_OUT ? p.W_unpool : job.phase == FEW_DOWN ? p.W_down : up ? p.W_up : p.W_gate;
+    return static_cast<const uint8_t*>(w) + first_row(c) * row_bytes();
   }
   __device__ __forceinline__ const uint8_t* scales(const FewChunks& c, int i) const {
-    const uint8_t* s = PHASE == FEW_DOWN ? p.s_down : i < 16 ? p.s_gate : p.s_up;
-    return s + (first_row(c) + (PHASE == FEW_DOWN ? i : i & 15)) * (K / 16);
+    const uint8_t* s = job.phase == FEW_DOWN ? p.s_down : i < 16 ? p.s_gate : p.s_up;
+    return s + (first_row(c) + (gate_up() ? i & 15 : i)) * (job.K / 16);
   }
-  __device__ __forceinline__ bool has_row(const FewChunks& c, int i) const {
-    return (PHASE == FEW_GATE_UP ? (i & 15) : i) < c.len;
-  }
+  // whether place i of a stage (gate/up: 0.. gate, 16.. up) holds a row of the chunk
+  __device__ __forceinline__ bool has_row(const FewChunks& c, int i) const { return (gate_up() ? i & 15 : i) < c.len; }
   __device__ __forceinline__ int tokens(const FewChunks& c) const {
-    return kExperts ? r.first[c.d + 1] - r.first[c.d] : p.T;
+    return experts() ? r.first[c.d + 1] - r.first[c.d] : p.T;
   }
   __device__ __forceinline__ const uint8_t* activation(const FewChunks& c, int j) const {
-    const void* x;
-    if constexpr (PHASE == FEW_IN) {
-      x = xin + static_cast<int64_t>(j) * K;
-    } else if constexpr (PHASE == FEW_GATE_UP) {
-      x = static_cast<const TZ*>(p.z) + static_cast<int64_t>(r.pair[r.first[c.d] + j] / p.k) * K;
-    } else if constexpr (PHASE == FEW_DOWN) {
-      x = static_cast<const TZ*>(p.h) + static_cast<int64_t>(r.first[c.d] + j) * K;
-    } else {
-      x = static_cast<const TA*>(p.c) + static_cast<int64_t>(j) * K;
-    }
-    return static_cast<const uint8_t*>(x);
+    const void* x = job.phase <= FEW_POOL ? static_cast<const void*>(xin) : gate_up() ? p.z
+                  : job.phase == FEW_DOWN ? p.h : p.c;
+    const int row = gate_up() ? r.token[r.first[c.d] + j] : job.phase == FEW_DOWN ? r.first[c.d] + j : j;
+    return static_cast<const uint8_t*>(x) + row * (job.K * static_cast<int64_t>(sizeof(TA)));
   }
 };
 
-// One producer warp's copies of a phase: warp 0 the activations (and NVFP4 block scales), once
+// One producer warp's copies of a job: warp 0 the activations (and NVFP4 block scales), once
 // `ready` (the barrier before this phase; nullptr: nothing to wait for) has passed; the others
 // each every third weight row, as far ahead as the ring is free. A stage's addresses advance by
 // constants from those of the chunk, so that a copy costs a few instructions.
-template <typename TA, bool FP4, int PHASE>
-__device__ __forceinline__ void few_produce(const FewSource<TA, FP4, PHASE>& q, FewChunks c, FewRing& ring,
-                                            const uint32_t* ready, volatile int* abort, int pw, int lane) {
-  constexpr int kFormat = FewSource<TA, FP4, PHASE>::kFormat;
-  using G = FewGeo<kFormat>;
+template <typename TA, int FORMAT>
+__device__ __forceinline__ void few_produce(const FewSource<TA, FORMAT>& q, FewRing& ring, const uint32_t* ready,
+                                            volatile int* abort, int pw, int lane) {
+  using G = FewGeo<FORMAT>;
   constexpr int kWeightWarps = kFewProducers - 1;
   constexpr int kMine = (kFewRows + kWeightWarps - 1) / kWeightWarps;
   const FewArgs& p = q.p;
-  const int K = q.K;
+  const int K = q.job.K;
+  FewChunks c(q.job.U, q.job.group, q.job.most);
   if (pw == 0 && ready != nullptr) {
-    if (lane == 0) few_poll(ready, gridDim.x, abort, p.status, 0xB00u + PHASE);
+    if (lane == 0) few_poll(ready, gridDim.x, abort, p.status, 0xB00u + q.job.phase);
     __syncwarp();
   }
   for (; !c.done(); c.next()) {
@@ -430,10 +462,11 @@ __device__ __forceinline__ void few_produce(const FewSource<TA, FP4, PHASE>& q, 
       const uint8_t* x = q.activation(c, min(lane, n - 1));  // lane j: token j's row
       // block scales: four 16-byte pieces of a row's 64 bytes a stage, a row per four lanes
       const uint8_t* sc[4];
-      if constexpr (kFormat == FEW_NVFP4) {
+      if constexpr (FORMAT == FEW_NVFP4) {
 #pragma unroll
         for (int a = 0; a < 4; ++a) sc[a] = q.scales(c, min(8 * a + (lane >> 2), kFewRows - 1)) + 16 * (lane & 3);
       }
+#pragma unroll 1
       for (int k0 = 0; k0 < K; k0 += G::kc) {
         const int kn = min(G::kc, K - k0);
         // (a wait that gave up: no copies; the arrivals go on so that nobody waits for them)
@@ -441,58 +474,56 @@ __device__ __forceinline__ void few_produce(const FewSource<TA, FP4, PHASE>& q, 
         if (__all_sync(0xffffffffu, ok)) {
           const uint32_t st = ring.addr();
           const int bytes = kn * static_cast<int>(G::act_bytes / G::kc);
+#pragma unroll 1
           for (int j = 0; j < n; ++j) {
             const uint8_t* xj = reinterpret_cast<const uint8_t*>(
                 __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x), j));
 #pragma unroll
-            for (int o = 16 * lane; o < static_cast<int>(G::act_bytes); o += 512)
-              if (o < bytes) cp_async16(st + G::xoff + G::xstride * j + o, xj + o);
+            for (int o = 0; o < static_cast<int>(G::act_bytes); o += 512)
+              cp_async16_if(o + 16 * lane < bytes, st + G::xoff + G::xstride * j + o + 16 * lane, xj + o + 16 * lane);
           }
-          if constexpr (kFormat == FEW_NVFP4) {
+          if constexpr (FORMAT == FEW_NVFP4) {
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
               const int i = 8 * a + (lane >> 2);
-              if (q.has_row(c, i) && 16 * (lane & 3) < kn / 16)
-                cp_async16(st + G::soff + G::sstride * i + 16 * (lane & 3), sc[a]);
+              cp_async16_if(q.has_row(c, i) && 16 * (lane & 3) < kn / 16,
+                            st + G::soff + G::sstride * i + 16 * (lane & 3), sc[a]);
             }
           }
         }
         cp_async_arrive(ring.full());
         ring.next();
         x += G::act_bytes;
-        if constexpr (kFormat == FEW_NVFP4) {
+        if constexpr (FORMAT == FEW_NVFP4) {
 #pragma unroll
           for (int a = 0; a < 4; ++a) sc[a] += G::kc / 16;
         }
       }
     } else {
-      // rows i = pw - 1 + kWeightWarps * m; two runs of consecutive rows: before and after `cut`
-      // (router / pooler; gate / up), whose distances are the matrix' row bytes
-      const int cut = PHASE == FEW_GATE_UP ? 16 : PHASE == FEW_IN ? max(0, min(kFewRows, p.E - c.f)) : kFewRows;
+      // places i = pw - 1 + kWeightWarps * m; from 16 on (gate/up) of the other matrix
       const int64_t step = q.row_bytes();
-      const uint8_t* w0 = q.row(c, 0) + 16 * lane;
-      const uint8_t* w1 = cut < kFewRows ? q.row(c, cut) - cut * step + 16 * lane : w0;
+      const uint8_t* w0 = q.row(c, false) + (pw - 1) * step + 16 * lane;
+      const uint8_t* w1 = q.gate_up() ? q.row(c, true) + (pw - 1 - 16) * step + 16 * lane : w0;
       uint32_t mask = 0;
 #pragma unroll
       for (int m = 0; m < kMine; ++m) {
         const int i = pw - 1 + kWeightWarps * m;
         if (i < kFewRows && q.has_row(c, i)) mask |= 1u << m;
       }
+#pragma unroll 1
       for (int k0 = 0; k0 < K; k0 += G::kc) {
-        const int bytes = min(G::kc, K - k0) * static_cast<int>(G::row_bytes) / G::kc;
+        const int bytes = min(G::kc, K - k0) * static_cast<int>(G::row_bytes) / G::kc - 16 * lane;
         const bool ok = mbar_wait(ring.empty(), ring.phase ^ 1u, abort, p.status, 0xA00u + ring.stage);
         if (__all_sync(0xffffffffu, ok)) {
           const uint32_t st = ring.addr() + 16 * lane + G::wstride * (pw - 1);
-          const uint8_t* a0 = w0 + (pw - 1) * step;
-          const uint8_t* a1 = w1 + (pw - 1) * step;
+          const uint8_t* a0 = w0;
+          const uint8_t* a1 = w1;
 #pragma unroll
           for (int m = 0; m < kMine; ++m) {
-            const uint8_t* a = pw - 1 + kWeightWarps * m < cut ? a0 : a1;
-            if (mask & (1u << m)) {
+            const uint8_t* a = pw - 1 + kWeightWarps * m < 16 ? a0 : a1;
 #pragma unroll
-              for (int o = 0; o < static_cast<int>(G::row_bytes); o += 512)
-                if (o + 16 * lane < bytes) cp_async16(st + kWeightWarps * m * G::wstride + o, a + o);
-            }
+            for (int o = 0; o < static_cast<int>(G::row_bytes); o += 512)
+              cp_async16_if((mask >> m & 1u) && o < bytes, st + kWeightWarps * m * G::wstride + o, a + o);
             a0 += kWeightWarps * step;
             a1 += kWeightWarps * step;
           }
@@ -506,8 +537,11 @@ __device__ __forceinline__ void few_produce(const FewSource<TA, FP4, PHASE>& q, 
   }
 }
 
-// ---- consumers --------------------------------------------------------------------------
-__device__ __forceinline__ void few_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kFewConsumers) : "memory"); }
+// ---- products ---------------------------------------------------------------------------
+// barriers over the product warps, the store warps, both with the producers
+__device__ __forceinline__ void few_sync_products() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kFewWarps) : "memory"); }
+__device__ __forceinline__ void few_sync_store() { asm volatile("bar.sync 2, %0;" ::"n"(32 * kFewStore) : "memory"); }
+__device__ __forceinline__ void few_sync_all() { asm volatile("bar.sync 3, %0;" ::"n"(kFewThreads) : "memory"); }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -528,11 +562,27 @@ __device__ __forceinline__ float4 as_float4(uint4 v) {
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
 
+// The two buffers of partial sums between product and store warps: [warp][token][row], the
+// tokens 33 floats apart.
+struct FewRed {
+  uint32_t bar0;  // full barriers, then free ones
+  float* base;
+  int buf;
+  uint32_t phase;
+  __device__ __forceinline__ uint32_t full() const { return bar0 + 8u * buf; }
+  __device__ __forceinline__ uint32_t free() const { return bar0 + 16u + 8u * buf; }
+  __device__ __forceinline__ float* red() const { return base + kFewRedFloats * buf; }
+  __device__ __forceinline__ void next() {
+    buf ^= 1;
+    if (buf == 0) phase ^= 1u;
+  }
+};
+
 // One chunk's products: the stages of 32 weight rows and n activation rows, this warp's share
-// of K; afterwards red[warp][token][row] (rows 33 floats apart) holds the warp's sums.
+// of K; the warp's sums go to the next buffer of partial sums.
 template <int FORMAT>
 __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int K, int n, int wc, int lane,
-                                            volatile int* abort, float* red) {
+                                            volatile int* abort, FewRed& out) {
   using G = FewGeo<FORMAT>;
   const int g = lane >> 2, t = lane & 3;
   const int gx = min(g, n - 1);  // token rows past n are not staged (their columns are not used)
@@ -549,7 +599,7 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int
     if constexpr (FORMAT == FEW_BF16) {
       const uint32_t w = st + g * G::wstride + t * 16u, x = st + G::xoff + gx * G::xstride + t * 16u;
       const uint32_t r8 = 8u * G::wstride;
-#pragma unroll 2
+#pragma unroll 1
       for (int s = wc; s < kn / 32; s += kFewWarps) {  // 32 elements = 64 bytes of each row
         const uint32_t o = 64u * s;
         const uint4 b = lds128(x + o), a0 = lds128(w + o), a1 = lds128(w + r8 + o), a2 = lds128(w + 2 * r8 + o),
@@ -562,6 +612,7 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int
     } else if constexpr (FORMAT == FEW_NVFP4) {
       const uint32_t w = st + g * G::wstride + t * 8u, x = st + G::xoff + gx * G::xstride + t * 32u;
       const uint32_t sc = st + G::soff + g * G::sstride;
+#pragma unroll 1
       for (int s = wc; s < kn / 64; s += kFewWarps) {  // 64 elements; this lane's 16-weight block: t
         const uint4 x0 = lds128(x + 128u * s), x1 = lds128(x + 128u * s + 16u);
         const uint32_t xv[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
@@ -586,7 +637,7 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int
       }
     } else {
       const uint32_t w = st + lane * G::wstride, x = st + G::xoff;
-#pragma unroll 2
+#pragma unroll 1
       for (int s = wc; s < kn / 4; s += kFewWarps) {
         const float4 a = as_float4(lds128(w + 16u * s));
 #pragma unroll
@@ -601,7 +652,9 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int
     if (lane == 0) mbar_arrive(ring.empty());
     ring.next();
   }
-  float* mine = red + wc * 8 * 33;
+  mbar_wait(out.free(), out.phase ^ 1u, abort, p.status, 0xD00u);
+  __syncwarp();
+  float* mine = out.red() + wc * 8 * 33;
   if constexpr (FORMAT == FEW_F32) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) mine[j * 33 + lane] = acc[j];
@@ -609,39 +662,79 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int
 #pragma unroll
     for (int i = 0; i < 8; ++i) mine[(2 * t + (i & 1)) * 33 + 16 * (i >> 2) + 8 * ((i >> 1) & 1) + g] = acc[i];
   }
+  __syncwarp();
+  if (lane == 0) mbar_arrive(out.full());
+  out.next();
 }
 
-// The warps' sums of (token, row), in warp order.
+// The warps' sums of (token, row), in a fixed order.
 __device__ __forceinline__ float few_sum(const float* red, int token, int row) {
-  float v = 0.0f;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int w = 0; w < kFewWarps; ++w) v += red[(w * 8 + token) * 33 + row];
-  return v;
+  for (int w = 0; w < kFewWarps; ++w) v[w & 3] += red[(w * 8 + token) * 33 + row];
+  return (v[0] + v[1]) + (v[2] + v[3]);
 }
 
 __device__ __forceinline__ float few_silu(float a) { return a / (1.0f + expf(-a)); }
 
-// Sum over the consumer threads, the same on each (part: 32 floats).
+// Sum over the product warps' threads, the same on each (part: 32 floats).
 __device__ __forceinline__ float few_block_sum(float v, float* part, int wc, int lane) {
   v = warp_sum(v);
-  few_sync();
+  few_sync_products();
   if (lane == 0) part[wc] = v;
-  few_sync();
+  few_sync_products();
   return warp_sum(lane < kFewWarps ? part[lane] : 0.0f);
 }
 
-// Centred RMSNorm of one row by the consumers: dst = src / sqrt(mean(src^2) + eps) * (1 + w).
+// Centred RMSNorm of one row by the product warps: dst = src / sqrt(mean(src^2) + eps) * (1 + w).
 template <typename TS, typename TG, typename TD>
 __device__ __forceinline__ void few_norm_row(const TS* src, const TG* w, TD* dst, int n, float eps, float* part,
                                              int tid) {
   float s = 0.0f;
-  for (int i = tid; i < n; i += kFewConsumers) {
+  for (int i = tid; i < n; i += 32 * kFewWarps) {
     const float v = to_f32(src[i]);
     s = fmaf(v, v, s);
   }
   const float scale = 1.0f / sqrtf(few_block_sum(s, part, tid >> 5, tid & 31) / static_cast<float>(n) + eps);
-  for (int i = tid; i < n; i += kFewConsumers) dst[i] = from_f32<TD>(to_f32(src[i]) * scale * (1.0f + to_f32(w[i])));
+  for (int i = tid; i < n; i += 32 * kFewWarps) dst[i] = from_f32<TD>(to_f32(src[i]) * scale * (1.0f + to_f32(w[i])));
 }
+
+// c = sum_j g_j y_j / rms_j (1 + gamma) by the product warps, each CTA a slice of it.
+template <typename TA>
+__device__ __forceinline__ void few_combine(const FewArgs& p, const FewRoute& route, float* scale_s, int wc, int lane,
+                                            int tid) {
+  const int T = p.T, L = p.L, k = p.k, nd = route.distinct, rows = nd * L;
+  const TA* gamma = static_cast<const TA*>(p.gamma);
+  // every pair's weight over its root mean square, from the CTAs that hold its rows
+  for (int a = wc; a < T * k; a += kFewWarps) {
+    const int pos = route.pos[a], e = route.expert[a];
+    int d = 0;
+    for (int i = lane; i < nd; i += 32)
+      if (route.ids[i] == e) d = i;
+    d = __reduce_max_sync(0xffffffffu, d);
+    const int c0 = few_owner(rows, d * L), c1 = few_owner(rows, (d + 1) * L - 1);
+    float s = 0.0f;
+    for (int i = c0 + lane; i <= c1; i += 32)  // (with fewer rows than CTAs, some have none)
+      if (few_share(rows, i) < few_share(rows, i + 1)) s += __ldcg(p.ss + static_cast<int64_t>(pos) * kFewGridMax + i);
+    s = warp_sum(s);
+    if (lane == 0) scale_s[a] = route.weight[a] / sqrtf(s / static_cast<float>(L) + p.eps);
+  }
+  few_sync_products();
+  for (int i = blockIdx.x * (32 * kFewWarps) + tid; i < T * L; i += gridDim.x * (32 * kFewWarps)) {
+    const int t = i / L, f = i - t * L;
+    float acc = 0.0f;
+#pragma unroll 8
+    for (int j = 0; j < k; ++j) {
+      const int a = t * k + j;
+      const float gm = to_f32(gamma[(p.gamma_shared ? 0 : static_cast<int64_t>(route.expert[a]) * L) + f]);
+      acc = fmaf(scale_s[a] * (1.0f + gm), __ldcg(p.y + static_cast<int64_t>(route.pos[a]) * L + f), acc);
+    }
+    static_cast<TA*>(p.c)[i] = from_f32<TA>(acc);
+  }
+}
+
+// grid barriers, by what they say is done
+enum FewBarrier : int { FEW_XN = 0, FEW_LOGITS, FEW_Z, FEW_ZN, FEW_H, FEW_Y, FEW_C, FEW_F };
 
 // TA: activations, dense weights, gains and the output (bf16 or float). FP4: NVFP4 experts
 // (TA = bf16; z and h are f16).
@@ -652,203 +745,232 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_cons
   constexpr int EXPERT = FP4 ? FEW_NVFP4 : DENSE;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ FewRoute route;
-  __shared__ __align__(8) uint64_t bars[2 * kFewMaxStages];
+  __shared__ __align__(8) uint64_t bars[2 * kFewMaxStages + 4];
   __shared__ float part[32];
   __shared__ float scale_s[kFewAssign];
   __shared__ int abort_flag;
   volatile int* abort = &abort_flag;
-  float* red = reinterpret_cast<float*>(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int T = p.T, D = p.D, L = p.L, I = p.I, E = p.E, k = p.k;
+  const int T = p.T, D = p.D, L = p.L, I = p.I, E = p.E;
   FewRing ring{smem_u32(bars), smem_u32(smem) + kFewRedBytes, p.stages, 0, 0u, p.stage_bytes};
+  FewRed red{smem_u32(bars + 2 * kFewMaxStages), reinterpret_cast<float*>(smem), 0, 0u};
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(smem_u32(bars + s), 32 * kFewProducers);
       mbar_init(smem_u32(bars + kFewMaxStages + s), kFewWarps);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(red.bar0 + 8u * i, kFewWarps);
+      mbar_init(red.bar0 + 16u + 8u * i, kFewStore);
+    }
     abort_flag = 0;
     fence_mbar_init();
   }
+  if (threadIdx.x < 32) route.seen[threadIdx.x] = 0;
+  for (int i = threadIdx.x; i < kFewAssign; i += kFewThreads) route.expert[i] = 0x7fffffff;
   __syncthreads();
   auto counter = [&](int i) { return p.barrier + 32 * i; };
-  const TA* xin = p.ffn_pre_gain != nullptr ? static_cast<const TA*>(p.xn) : static_cast<const TA*>(p.x);
-  auto route_ready = [] { asm volatile("bar.sync 2, %0;" ::"n"(kFewThreads) : "memory"); };
+  const bool pre = p.ffn_pre_gain != nullptr, zn = p.pre_norm_gain != nullptr;
+  const bool finish = p.ffn_post_gain != nullptr || p.residual_gate != nullptr;
+  const TA* xin = pre ? static_cast<const TA*>(p.xn) : static_cast<const TA*>(p.x);
 
+  // ------------------------------------------------------------------------- producers
   if (warp < kFewProducers) {
-    few_produce(FewSource<TA, FP4, FEW_IN>{p, route, xin, D}, FewChunks(E + L, E + L, kFewRows), ring,
-                p.ffn_pre_gain != nullptr ? counter(0) : nullptr, abort, warp, lane);
-    route_ready();
-    const int nd = route.distinct;
-    few_produce(FewSource<TA, FP4, FEW_GATE_UP>{p, route, xin, L},
-                FewChunks(static_cast<int64_t>(nd) * I, I, kFewRows / 2), ring,
-                counter(p.pre_norm_gain != nullptr ? 2 : 1), abort, warp, lane);
-    few_produce(FewSource<TA, FP4, FEW_DOWN>{p, route, xin, I}, FewChunks(static_cast<int64_t>(nd) * L, L, kFewRows),
-                ring, counter(3), abort, warp, lane);
-    few_produce(FewSource<TA, FP4, FEW_OUT>{p, route, xin, L}, FewChunks(D, D, kFewRows), ring, counter(5),
-                abort, warp, lane);
+#pragma unroll 1
+    for (int ph = FEW_ROUTER; ph <= FEW_OUT; ++ph) {
+      if (ph == FEW_GATE_UP) few_sync_all();
+      const FewJob job = few_job(p, ph, route.distinct);
+      const uint32_t* ready = ph <= FEW_POOL ? (pre ? counter(FEW_XN) : nullptr)
+                              : counter(ph == FEW_GATE_UP ? (zn ? FEW_ZN : FEW_Z) : ph == FEW_DOWN ? FEW_H : FEW_C);
+      if (FP4 && (ph == FEW_GATE_UP || ph == FEW_DOWN))
+        few_produce(FewSource<TA, EXPERT>{p, route, xin, job}, ring, ready, abort, warp, lane);
+      else
+        few_produce(FewSource<TA, DENSE>{p, route, xin, job}, ring, ready, abort, warp, lane);
+    }
     cp_async_wait_all();  // nothing in flight when the CTA leaves, also after a wait that gave up
     return;
   }
 
-  const int wc = warp - kFewProducers, tid = threadIdx.x - 32 * kFewProducers;
-  // this CTA's part of barrier i is done: its global writes are visible to whoever sees the count
-  auto arrive = [&](int i) {
-    __threadfence();
-    few_sync();
-    if (tid == 0) red_release_u32(counter(i), 1u);
-  };
-  auto wait = [&](int i) {
-    if (tid == 0) few_poll(counter(i), gridDim.x, abort, p.status, 0xF00u + i);
-    few_sync();
-  };
-  // one phase's chunks; store(chunk, token, lane's row, sum) runs on warp `token` of the consumers
-  auto products = [&](auto format, FewChunks c, int K, bool by_expert, auto store) {
-    for (; !c.done(); c.next()) {
-      const int n = by_expert ? route.first[c.d + 1] - route.first[c.d] : T;
-      few_consume<decltype(format)::value>(p, ring, K, n, wc, lane, abort, red);
-      few_sync();
-      for (int j = wc; j < n; j += kFewWarps) store(c, j, few_sum(red, j, lane));
-      few_sync();
-    }
-  };
-  using Dense = std::integral_constant<int, DENSE>;
-  using Expert = std::integral_constant<int, EXPERT>;
-
-  if (p.ffn_pre_gain != nullptr) {
-    for (int t = blockIdx.x; t < T; t += gridDim.x)
-      few_norm_row(static_cast<const TA*>(p.x) + static_cast<int64_t>(t) * D, static_cast<const TA*>(p.ffn_pre_gain),
-                   static_cast<TA*>(p.xn) + static_cast<int64_t>(t) * D, D, p.ffn_pre_eps, part, tid);
-    arrive(0);
-  }
-  products(Dense{}, FewChunks(E + L, E + L, kFewRows), D, false, [&](const FewChunks& c, int j, float v) {
-    const int r = c.f + lane;
-    if (lane < c.len) {
-      if (r < E) p.logits[static_cast<int64_t>(j) * E + r] = v;
-      else static_cast<TZ*>(p.z)[static_cast<int64_t>(j) * L + r - E] = from_f32<TZ>(v);
-    }
-  });
-  arrive(1);
-  wait(1);
-  if (p.pre_norm_gain != nullptr) {
-    TZ* z = static_cast<TZ*>(p.z);
-    for (int t = blockIdx.x; t < T; t += gridDim.x)
-      few_norm_row(z + static_cast<int64_t>(t) * L, static_cast<const TA*>(p.pre_norm_gain),
-                   z + static_cast<int64_t>(t) * L, L, p.pre_norm_eps, part, tid);
-    arrive(2);
-  }
-  few_route(p, route, wc, kFewWarps, lane);
-  few_sync();
-  few_lists(p, route, tid, kFewConsumers, [] { few_sync(); });
-  route_ready();
-  const int nd = route.distinct;
-  products(Expert{}, FewChunks(static_cast<int64_t>(nd) * I, I, kFewRows / 2), L, true,
-           [&](const FewChunks& c, int j, float v) {
-             const float u = __shfl_down_sync(0xffffffffu, v, 16);
-             float mg = 1.0f, mu = 1.0f;
-             if constexpr (FP4) {
-               mg = p.m_gate[route.ids[c.d]];
-               mu = p.m_up[route.ids[c.d]];
-             }
-             if (lane < c.len)
-               static_cast<TZ*>(p.h)[static_cast<int64_t>(route.first[c.d] + j) * I + c.f + lane] =
-                   from_f32<TZ>(few_silu(v * mg) * (u * mu));
-           });
-  arrive(3);
-  {
-    // sums of squares of the rows this CTA computed of each position (lane 0 of the token's warp)
-    float ss = 0.0f;
-    int ss_d = -1;
-    auto flush = [&](int j) {
-      if (ss_d >= 0 && lane == 0) p.ss[static_cast<int64_t>(route.first[ss_d] + j) * kFewGridMax + blockIdx.x] = ss;
+  const TA* gamma = static_cast<const TA*>(p.gamma);
+  const TA* post = static_cast<const TA*>(p.ffn_post_gain);
+  // ------------------------------------------------------------------------- store warps
+  if (warp < kFewProducers + kFewStore) {
+    const int ws = warp - kFewProducers, tid = threadIdx.x - 32 * kFewProducers;
+    // this CTA's part of barrier i is done
+    auto arrive = [&](int i) {
+      few_sync_store();
+      if (tid == 0) red_release_u32(counter(i), 1u);  // (cumulative: orders the warps' writes too)
     };
-    const TA* gamma = static_cast<const TA*>(p.gamma);
-    const int64_t dn = static_cast<int64_t>(nd) * L;
-    FewChunks c(dn, L, kFewRows);
-    int last_n = 0;
-    for (; !c.done(); c.next()) {
-      const int n = route.first[c.d + 1] - route.first[c.d], e = route.ids[c.d];
-      few_consume<EXPERT>(p, ring, I, n, wc, lane, abort, red);
-      few_sync();
-      if (c.d != ss_d) {
-        if (wc < last_n) flush(wc);
-        ss = 0.0f;
-        ss_d = c.d;
-        last_n = n;
+    // the sums of a chunk: store(chunk, token, lane's row, sum) on warp token % kFewStore
+    auto chunk = [&](const FewChunks& c, int n, auto store) {
+      mbar_wait(red.full(), red.phase, abort, p.status, 0xE00u);
+      __syncwarp();
+#pragma unroll 1
+      for (int j = ws; j < n; j += kFewStore) store(c, j, few_sum(red.red(), j, lane));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(red.free());
+      red.next();
+    };
+    auto each = [&](int ph, auto store) {
+      const FewJob job = few_job(p, ph, route.distinct);
+#pragma unroll 1
+      for (FewChunks c(job.U, job.group, job.most); !c.done(); c.next())
+        chunk(c, ph == FEW_GATE_UP || ph == FEW_DOWN ? route.first[c.d + 1] - route.first[c.d] : T, store);
+    };
+    each(FEW_ROUTER, [&](const FewChunks& c, int j, float v) {
+      if (lane < c.len) p.logits[static_cast<int64_t>(j) * E + c.f + lane] = v;
+    });
+    arrive(FEW_LOGITS);
+    {
+      // store z and select the experts, whichever can be done first: in a large layer the logits
+      // of all CTAs are there long before the pooler's rows, in a small one the rows are
+      FewChunks c(L, L, kFewRows);
+      bool routed = false;
+#pragma unroll 1
+      while (!routed || !c.done()) {
+        // (votes: the lanes' reads may differ)
+        if (!routed && (c.done() || __all_sync(0xffffffffu, ld_acquire_u32(counter(FEW_LOGITS)) >= gridDim.x))) {
+          few_poll(counter(FEW_LOGITS), gridDim.x, abort, p.status, 0xF00u + FEW_LOGITS);
+          __syncwarp();
+#pragma unroll 1
+          for (int t = ws; t < T; t += kFewStore) few_route(p, route, t, lane);
+          routed = true;
+        } else if (routed || __all_sync(0xffffffffu, *abort != 0 || mbar_try_wait(red.full(), red.phase))) {
+          chunk(c, T, [&](const FewChunks& cc, int j, float v) {
+            if (lane < cc.len) static_cast<TZ*>(p.z)[static_cast<int64_t>(j) * L + cc.f + lane] = from_f32<TZ>(v);
+          });
+          c.next();
+        }
       }
-      if (wc < n) {
-        float y = few_sum(red, wc, lane);
+    }
+    arrive(FEW_Z);
+    few_lists(p, route, tid, 32 * kFewStore);
+    few_sync_all();
+    each(FEW_GATE_UP, [&](const FewChunks& c, int j, float v) {
+      const float u = __shfl_down_sync(0xffffffffu, v, 16);
+      float mg = 1.0f, mu = 1.0f;
+      if constexpr (FP4) {
+        mg = p.m_gate[route.ids[c.d]];
+        mu = p.m_up[route.ids[c.d]];
+      }
+      if (lane < c.len)
+        static_cast<TZ*>(p.h)[static_cast<int64_t>(route.first[c.d] + j) * I + c.f + lane] =
+            from_f32<TZ>(few_silu(v * mg) * (u * mu));
+    });
+    arrive(FEW_H);
+    {
+      // sums of squares of the rows this CTA computes of each position: tokens ws and ws + 4 of
+      // the current expert
+      float ss[2] = {0.0f, 0.0f};
+      int ss_d = -1;
+      auto flush = [&]() {
+        if (ss_d < 0) return;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int pos = route.first[ss_d] + ws + kFewStore * h;
+          if (lane == 0 && pos < route.first[ss_d + 1]) p.ss[static_cast<int64_t>(pos) * kFewGridMax + blockIdx.x] = ss[h];
+          ss[h] = 0.0f;
+        }
+      };
+      each(FEW_DOWN, [&](const FewChunks& c, int j, float y) {
+        if (c.d != ss_d) flush();
+        ss_d = c.d;
+        const int e = route.ids[c.d];
         if constexpr (FP4) y *= p.m_down[e];
         float u = 0.0f;
         if (lane < c.len) {
-          p.y[static_cast<int64_t>(route.first[c.d] + wc) * L + c.f + lane] = y;
+          p.y[static_cast<int64_t>(route.first[c.d] + j) * L + c.f + lane] = y;
           u = y;
           if (p.norm_mode == 1)
             u *= 1.0f + to_f32(gamma[(p.gamma_shared ? 0 : static_cast<int64_t>(e) * L) + c.f + lane]);
         }
-        ss += warp_sum(u * u);
+        const float s = warp_sum(u * u);
+        if (j < kFewStore) ss[0] += s;
+        else ss[1] += s;
+      });
+      flush();
+      arrive(FEW_Y);
+    }
+    float ssf[2] = {0.0f, 0.0f};  // of this CTA's rows of tokens ws and ws + 4
+    each(FEW_OUT, [&](const FewChunks& c, int j, float v) {
+      const int64_t o = static_cast<int64_t>(j) * D + c.f + lane;
+      if (!finish) {
+        if (lane < c.len) static_cast<TA*>(p.out)[o] = from_f32<TA>(v);
+        return;
       }
-      few_sync();
-    }
-    if (wc < last_n) flush(wc);
-    arrive(4);
-    wait(4);
-    // phase 4: every pair's weight over its root mean square, from the CTAs that hold its rows
-    for (int a = wc; a < T * k; a += kFewWarps) {
-      const int pos = route.pos[a];
-      int d = 0;
-      for (int i = lane; i < nd; i += 32)
-        if (route.first[i] <= pos) d = i;
-      d = __reduce_max_sync(0xffffffffu, d);
-      const int c0 = few_owner(dn, static_cast<int64_t>(d) * L), c1 = few_owner(dn, static_cast<int64_t>(d + 1) * L - 1);
-      float s = 0.0f;
-      for (int i = c0 + lane; i <= c1; i += 32)  // (with fewer rows than CTAs, some have none)
-        if (dn * i / gridDim.x < dn * (i + 1) / gridDim.x) s += __ldcg(p.ss + static_cast<int64_t>(pos) * kFewGridMax + i);
-      s = warp_sum(s);
-      if (lane == 0) scale_s[a] = route.weight[a] / sqrtf(s / static_cast<float>(L) + p.eps);
-    }
-    few_sync();
-    for (int i = blockIdx.x * kFewConsumers + tid; i < T * L; i += gridDim.x * kFewConsumers) {
-      const int t = i / L, f = i - t * L;
-      float acc = 0.0f;
-#pragma unroll 8
-      for (int j = 0; j < k; ++j) {
-        const int a = t * k + j;
-        const float gm = to_f32(gamma[(p.gamma_shared ? 0 : static_cast<int64_t>(route.expert[a]) * L) + f]);
-        acc = fmaf(scale_s[a] * (1.0f + gm), __ldcg(p.y + static_cast<int64_t>(route.pos[a]) * L + f), acc);
+      float u = 0.0f;
+      if (lane < c.len) {
+        p.f[o] = v;
+        if (post != nullptr) u = v * (1.0f + to_f32(post[c.f + lane]));
       }
-      static_cast<TA*>(p.c)[i] = from_f32<TA>(acc);
+      const float s = warp_sum(u * u);
+      if (j < kFewStore) ssf[0] += s;
+      else ssf[1] += s;
+    });
+    if (finish) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (lane == 0 && ws + kFewStore * h < T) p.ssf[(ws + kFewStore * h) * kFewGridMax + blockIdx.x] = ssf[h];
+      arrive(FEW_F);
     }
-    arrive(5);
+    return;
   }
-  const bool finish = p.ffn_post_gain != nullptr || p.residual_gate != nullptr;
-  const TA* post = static_cast<const TA*>(p.ffn_post_gain);
-  float ssf = 0.0f;  // of this CTA's rows of token wc
-  products(Dense{}, FewChunks(D, D, kFewRows), L, false, [&](const FewChunks& c, int j, float v) {
-    const int64_t o = static_cast<int64_t>(j) * D + c.f + lane;
-    if (!finish) {
-      if (lane < c.len) static_cast<TA*>(p.out)[o] = from_f32<TA>(v);
-      return;
+
+  // ------------------------------------------------------------------------- product warps
+  const int wc = warp - kFewProducers - kFewStore, tid = threadIdx.x - 32 * (kFewProducers + kFewStore);
+  constexpr int kProducts = 32 * kFewWarps;
+  auto arrive = [&](int i) {
+    few_sync_products();
+    if (tid == 0) red_release_u32(counter(i), 1u);
+  };
+  auto wait = [&](int i) {
+    if (tid == 0) few_poll(counter(i), gridDim.x, abort, p.status, 0xF00u + i);
+    few_sync_products();
+  };
+  if (pre) {
+    for (int t = blockIdx.x; t < T; t += gridDim.x)
+      few_norm_row(static_cast<const TA*>(p.x) + static_cast<int64_t>(t) * D, static_cast<const TA*>(p.ffn_pre_gain),
+                   static_cast<TA*>(p.xn) + static_cast<int64_t>(t) * D, D, p.ffn_pre_eps, part, tid);
+    arrive(FEW_XN);
+  }
+#pragma unroll 1
+  for (int ph = FEW_ROUTER; ph <= FEW_OUT; ++ph) {
+    if (ph == FEW_GATE_UP) {
+      if (zn) {
+        wait(FEW_Z);
+        TZ* z = static_cast<TZ*>(p.z);
+        for (int t = blockIdx.x; t < T; t += gridDim.x)
+          few_norm_row(z + static_cast<int64_t>(t) * L, static_cast<const TA*>(p.pre_norm_gain),
+                       z + static_cast<int64_t>(t) * L, L, p.pre_norm_eps, part, tid);
+        arrive(FEW_ZN);
+      }
+      few_sync_all();
     }
-    float u = 0.0f;
-    if (lane < c.len) {
-      p.f[o] = v;
-      if (post != nullptr) u = v * (1.0f + to_f32(post[c.f + lane]));
+    if (ph == FEW_OUT) {
+      wait(FEW_Y);
+      few_combine<TA>(p, route, scale_s, wc, lane, tid);
+      arrive(FEW_C);
     }
-    ssf += warp_sum(u * u);
-  });
+    const FewJob job = few_job(p, ph, route.distinct);
+    const bool experts = ph == FEW_GATE_UP || ph == FEW_DOWN;
+#pragma unroll 1
+    for (FewChunks c(job.U, job.group, job.most); !c.done(); c.next()) {
+      const int n = experts ? route.first[c.d + 1] - route.first[c.d] : T;
+      if (FP4 && experts) few_consume<EXPERT>(p, ring, job.K, n, wc, lane, abort, red);
+      else few_consume<DENSE>(p, ring, job.K, n, wc, lane, abort, red);
+    }
+  }
   if (!finish) return;
-  if (wc < T && lane == 0) p.ssf[wc * kFewGridMax + blockIdx.x] = ssf;
-  arrive(6);
-  wait(6);
-  // phase 6
+  wait(FEW_F);
+  // post norm and residual gate
   for (int t = wc; t < T; t += kFewWarps) {
     float s = 0.0f;
     for (int i = lane; i < static_cast<int>(gridDim.x); i += 32) s += __ldcg(p.ssf + t * kFewGridMax + i);
     s = warp_sum(s);
     if (lane == 0) scale_s[t] = 1.0f / sqrtf(s / static_cast<float>(D) + p.ffn_post_eps);
   }
-  few_sync();
-  for (int i = blockIdx.x * kFewConsumers + tid; i < T * D; i += gridDim.x * kFewConsumers) {
+  few_sync_products();
+  for (int i = blockIdx.x * kProducts + tid; i < T * D; i += gridDim.x * kProducts) {
     const int t = i / D, f = i - t * D;
     float v = __ldcg(p.f + i);
     if (post != nullptr) v *= (1.0f + to_f32(post[f])) * scale_s[t];
