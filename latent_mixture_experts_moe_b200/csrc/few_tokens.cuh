@@ -56,7 +56,7 @@ constexpr int kFewAssign = 8 * 32;    // most (token, expert) pairs: top_k <= 32
 constexpr int kFewGridMax = 192;      // CTAs a workspace has partial sums for
 constexpr int kFewProducers = 4;      // producer warps: one for activations, the others for weights
 constexpr int kFewStore = 4;          // store warps
-constexpr int kFewWarps = 16;         // product warps
+constexpr int kFewWarps = 8;          // product warps
 constexpr int kFewThreads = 32 * (kFewProducers + kFewStore + kFewWarps);
 constexpr int kFewRows = 32;          // weight rows of a stage (gate/up: 16 features of each)
 constexpr int kFewMaxStages = 16;
@@ -66,26 +66,42 @@ constexpr uint32_t kFewRedBytes = 2u * kFewRedFloats * 4u;    // two chunks'
 
 enum FewFormat : int { FEW_BF16 = 0, FEW_NVFP4 = 1, FEW_F32 = 2 };
 
-// How the stages of a product with weights of a format lie in shared memory: kc elements of K
-// per stage, so that every consumer warp has a share of each (its unit: 32 bf16 elements, 64
-// NVFP4, 4 float32); weight rows wstride bytes apart from offset 0, NVFP4 block scales sstride
-// apart from soff, activation rows xstride apart from xoff. The row distances keep the
-// consumers' reads free of bank conflicts: bf16 rows 64 bytes past a multiple of 128 (a quarter
-// warp reads 64 bytes of two rows), float rows 16 past it (eight lanes read one row each), codes
-// 32 (half a warp reads 32 bytes of four rows), scales an odd multiple of 16, f16 activations
-// beside codes 16 (32 bytes a lane, in two reads).
+// How the stages of a product with weights of a format lie in shared memory: at most kc elements
+// of K per stage, so that every product warp has a share of each (its unit: 32 bf16 elements,
+// 128 NVFP4, 4 float32); weight rows wstride bytes apart from offset 0, NVFP4 block scales
+// sstride apart from soff, activation rows xstride(n) apart from xoff. 2048 elements of NVFP4
+// rows are as many bytes as 512 of bf16, but each activation row then takes 4 KB: with more
+// than two tokens on an expert (rare) its stages hold less of K instead of more bytes.
+// The row distances keep the product warps' reads free of bank conflicts: bf16 rows 64 bytes
+// past a multiple of 128 (a quarter warp reads 64 bytes of two rows), and codes too, float rows
+// 16 past it (eight lanes read one row each), scales an odd multiple of 16; f16 activations
+// beside codes, of which a lane reads 64 bytes in four steps, have 16 spare bytes after every
+// 128 and rows 32 past a multiple of 128.
 template <int FORMAT>
 struct FewGeo {
-  static constexpr int kc = FORMAT == FEW_NVFP4 ? 1024 : FORMAT == FEW_BF16 ? 512 : 256;
-  static constexpr uint32_t row_bytes = FORMAT == FEW_NVFP4 ? kc / 2 : FORMAT == FEW_BF16 ? kc * 2 : kc * 4;
-  static constexpr uint32_t act_bytes = FORMAT == FEW_F32 ? kc * 4 : kc * 2;
-  static constexpr uint32_t wstride = row_bytes + (FORMAT == FEW_NVFP4 ? 32 : FORMAT == FEW_BF16 ? 64 : 16);
+  static constexpr int kc = FORMAT == FEW_NVFP4 ? 2048 : FORMAT == FEW_BF16 ? 512 : 256;
+  static constexpr int act_size = FORMAT == FEW_F32 ? 4 : 2;
+  static constexpr uint32_t row_bytes = FORMAT == FEW_NVFP4 ? kc / 2 : kc * act_size;
+  static constexpr uint32_t wstride = row_bytes + (FORMAT == FEW_F32 ? 16 : 64);
   static constexpr uint32_t soff = kFewRows * wstride;
   static constexpr uint32_t sstride = FORMAT == FEW_NVFP4 ? (kc / 16) | 16 : 0;
   static constexpr uint32_t xoff = soff + kFewRows * sstride;
-  static constexpr uint32_t xstride = act_bytes + (FORMAT == FEW_BF16 ? 64 : 16);
-  // bytes of a stage with n activation rows
-  static constexpr uint32_t bytes(int n) { return xoff + static_cast<uint32_t>(n) * xstride; }
+  // elements of K per stage, and the distance of activation rows, with n tokens
+  __host__ __device__ static constexpr int depth(int n) {
+    return FORMAT != FEW_NVFP4 || n <= 2 ? kc : n <= 4 ? kc / 2 : kc / 4;
+  }
+  __host__ __device__ static constexpr uint32_t xstride(int n) {
+    return static_cast<uint32_t>(FORMAT == FEW_NVFP4 ? depth(n) / 8 * 9 * act_size + 32
+                                                     : depth(n) * act_size + (FORMAT == FEW_BF16 ? 64 : 16));
+  }
+  // where byte a of an activation row's piece lies
+  __device__ static constexpr uint32_t xbyte(uint32_t a) { return FORMAT == FEW_NVFP4 ? a + a / 128 * 16 : a; }
+  // bytes of a stage that holds up to T tokens
+  static constexpr uint32_t bytes(int T) {
+    uint32_t x = 0;
+    for (int n = 1; n <= T; ++n) x = n * xstride(n) > x ? n * xstride(n) : x;
+    return xoff + x;
+  }
 };
 
 struct FewArgs {
@@ -439,9 +455,9 @@ struct FewSource {
   }
 };
 
-// One producer warp's copies of a job: warp 0 the activations (and NVFP4 block scales), once
+// One producer warp's copies of a job: warp 0 the activations, once
 // `ready` (the barrier before this phase; nullptr: nothing to wait for) has passed; the others
-// each every third weight row, as far ahead as the ring is free. A stage's addresses advance by
+// each every third weight row (and a third of the block scales), as far ahead as the ring is free. A stage's addresses advance by
 // constants from those of the chunk, so that a copy costs a few instructions.
 template <typename TA, int FORMAT>
 __device__ __forceinline__ void few_produce(const FewSource<TA, FORMAT>& q, FewRing& ring, const uint32_t* ready,
@@ -457,47 +473,30 @@ __device__ __forceinline__ void few_produce(const FewSource<TA, FORMAT>& q, FewR
     __syncwarp();
   }
   for (; !c.done(); c.next()) {
+    const int n = q.tokens(c), kc = G::depth(n);
     if (pw == 0) {
-      const int n = q.tokens(c);
+      const uint32_t xstride = G::xstride(n);
       const uint8_t* x = q.activation(c, min(lane, n - 1));  // lane j: token j's row
-      // block scales: four 16-byte pieces of a row's 64 bytes a stage, a row per four lanes
-      const uint8_t* sc[4];
-      if constexpr (FORMAT == FEW_NVFP4) {
-#pragma unroll
-        for (int a = 0; a < 4; ++a) sc[a] = q.scales(c, min(8 * a + (lane >> 2), kFewRows - 1)) + 16 * (lane & 3);
-      }
 #pragma unroll 1
-      for (int k0 = 0; k0 < K; k0 += G::kc) {
-        const int kn = min(G::kc, K - k0);
+      for (int k0 = 0; k0 < K; k0 += kc) {
+        const int kn = min(kc, K - k0);
         // (a wait that gave up: no copies; the arrivals go on so that nobody waits for them)
         const bool ok = mbar_wait(ring.empty(), ring.phase ^ 1u, abort, p.status, 0xA00u + ring.stage);
         if (__all_sync(0xffffffffu, ok)) {
           const uint32_t st = ring.addr();
-          const int bytes = kn * static_cast<int>(G::act_bytes / G::kc);
+          const int bytes = kn * G::act_size;
 #pragma unroll 1
           for (int j = 0; j < n; ++j) {
             const uint8_t* xj = reinterpret_cast<const uint8_t*>(
                 __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x), j));
-#pragma unroll
-            for (int o = 0; o < static_cast<int>(G::act_bytes); o += 512)
-              cp_async16_if(o + 16 * lane < bytes, st + G::xoff + G::xstride * j + o + 16 * lane, xj + o + 16 * lane);
-          }
-          if constexpr (FORMAT == FEW_NVFP4) {
-#pragma unroll
-            for (int a = 0; a < 4; ++a) {
-              const int i = 8 * a + (lane >> 2);
-              cp_async16_if(q.has_row(c, i) && 16 * (lane & 3) < kn / 16,
-                            st + G::soff + G::sstride * i + 16 * (lane & 3), sc[a]);
-            }
+            const uint32_t dst = st + G::xoff + xstride * j;
+#pragma unroll 2
+            for (int a = 16 * lane; a - 16 * lane < bytes; a += 512) cp_async16_if(a < bytes, dst + G::xbyte(a), xj + a);
           }
         }
         cp_async_arrive(ring.full());
         ring.next();
-        x += G::act_bytes;
-        if constexpr (FORMAT == FEW_NVFP4) {
-#pragma unroll
-          for (int a = 0; a < 4; ++a) sc[a] += G::kc / 16;
-        }
+        x += kc * G::act_size;
       }
     } else {
       // places i = pw - 1 + kWeightWarps * m; from 16 on (gate/up) of the other matrix
@@ -510,9 +509,23 @@ __device__ __forceinline__ void few_produce(const FewSource<TA, FORMAT>& q, FewR
         const int i = pw - 1 + kWeightWarps * m;
         if (i < kFewRows && q.has_row(c, i)) mask |= 1u << m;
       }
+      // block scales, in 16-byte pieces (256 elements): eight a row, by all lanes of these warps
+      constexpr int kSc = FORMAT == FEW_NVFP4 ? (kFewRows * 8 + 32 * kWeightWarps - 1) / (32 * kWeightWarps) : 0;
+      const uint8_t* sc[kSc + 1];
+      uint32_t sdst[kSc + 1];
+      int sk[kSc + 1];  // first element of K a piece covers; past K: no piece
+      if constexpr (FORMAT == FEW_NVFP4) {
+#pragma unroll
+        for (int i = 0; i < kSc; ++i) {
+          const int a = (pw - 1) * 32 + lane + 32 * kWeightWarps * i, row = min(a >> 3, kFewRows - 1);
+          sc[i] = q.scales(c, row) + 16 * (a & 7);
+          sdst[i] = G::soff + G::sstride * row + 16 * (a & 7);
+          sk[i] = a < 8 * kFewRows && q.has_row(c, row) ? 256 * (a & 7) : 0x7fffffff;
+        }
+      }
 #pragma unroll 1
-      for (int k0 = 0; k0 < K; k0 += G::kc) {
-        const int bytes = min(G::kc, K - k0) * static_cast<int>(G::row_bytes) / G::kc - 16 * lane;
+      for (int k0 = 0; k0 < K; k0 += kc) {
+        const int kn = min(kc, K - k0), bytes = (FORMAT == FEW_NVFP4 ? kn / 2 : kn * G::act_size) - 16 * lane;
         const bool ok = mbar_wait(ring.empty(), ring.phase ^ 1u, abort, p.status, 0xA00u + ring.stage);
         if (__all_sync(0xffffffffu, ok)) {
           const uint32_t st = ring.addr() + 16 * lane + G::wstride * (pw - 1);
@@ -527,11 +540,15 @@ __device__ __forceinline__ void few_produce(const FewSource<TA, FORMAT>& q, FewR
             a0 += kWeightWarps * step;
             a1 += kWeightWarps * step;
           }
+#pragma unroll
+          for (int i = 0; i < kSc; ++i) cp_async16_if(sk[i] < kn, ring.addr() + sdst[i], sc[i]);
         }
         cp_async_arrive(ring.full());
         ring.next();
-        w0 += G::row_bytes;
-        w1 += G::row_bytes;
+        w0 += FORMAT == FEW_NVFP4 ? kc / 2 : kc * G::act_size;
+        w1 += FORMAT == FEW_NVFP4 ? kc / 2 : kc * G::act_size;
+#pragma unroll
+        for (int i = 0; i < kSc; ++i) sc[i] += kc / 16;
       }
     }
   }
@@ -548,14 +565,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
   return v;
 }
 __device__ __forceinline__ float4 as_float4(uint4 v) {
@@ -586,64 +598,79 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int
   using G = FewGeo<FORMAT>;
   const int g = lane >> 2, t = lane & 3;
   const int gx = min(g, n - 1);  // token rows past n are not staged (their columns are not used)
-  float acc[8];  // MMA: two 16-row tiles of 4; float32: this lane's row, 8 tokens
+  float acc[8];          // float32: this lane's row, 8 tokens
+  float chain[2][2][4];  // MMA: two 16-row tiles, each in two sums, so that fewer MMAs wait for one another
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
-  float(&lo)[4] = *reinterpret_cast<float(*)[4]>(&acc[0]);
-  float(&hi)[4] = *reinterpret_cast<float(*)[4]>(&acc[4]);
-  for (int k0 = 0; k0 < K; k0 += G::kc) {
-    const int kn = min(G::kc, K - k0);
+  for (int i = 0; i < 8; ++i) {
+    acc[i] = 0.0f;
+    chain[0][i >> 2][i & 3] = chain[1][i >> 2][i & 3] = 0.0f;
+  }
+  const int kc = G::depth(n);
+  const uint32_t xstride = G::xstride(n);
+#pragma unroll 1
+  for (int k0 = 0; k0 < K; k0 += kc) {
+    const int kn = min(kc, K - k0);
     mbar_wait(ring.full(), ring.phase, abort, p.status, 0xC00u + ring.stage);
     __syncwarp();
     const uint32_t st = ring.addr();
     if constexpr (FORMAT == FEW_BF16) {
-      const uint32_t w = st + g * G::wstride + t * 16u, x = st + G::xoff + gx * G::xstride + t * 16u;
+      const uint32_t w = st + g * G::wstride + t * 16u, x = st + G::xoff + gx * xstride + t * 16u;
       const uint32_t r8 = 8u * G::wstride;
-#pragma unroll 1
+#pragma unroll 2
       for (int s = wc; s < kn / 32; s += kFewWarps) {  // 32 elements = 64 bytes of each row
         const uint32_t o = 64u * s;
         const uint4 b = lds128(x + o), a0 = lds128(w + o), a1 = lds128(w + r8 + o), a2 = lds128(w + 2 * r8 + o),
                     a3 = lds128(w + 3 * r8 + o);
-        mma_bf16_16816(lo, a0.x, a1.x, a0.y, a1.y, b.x, b.y);
-        mma_bf16_16816(hi, a2.x, a3.x, a2.y, a3.y, b.x, b.y);
-        mma_bf16_16816(lo, a0.z, a1.z, a0.w, a1.w, b.z, b.w);
-        mma_bf16_16816(hi, a2.z, a3.z, a2.w, a3.w, b.z, b.w);
+        mma_bf16_16816(chain[0][0], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
+        mma_bf16_16816(chain[0][1], a2.x, a3.x, a2.y, a3.y, b.x, b.y);
+        mma_bf16_16816(chain[1][0], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+        mma_bf16_16816(chain[1][1], a2.z, a3.z, a2.w, a3.w, b.z, b.w);
       }
     } else if constexpr (FORMAT == FEW_NVFP4) {
-      const uint32_t w = st + g * G::wstride + t * 8u, x = st + G::xoff + gx * G::xstride + t * 32u;
-      const uint32_t sc = st + G::soff + g * G::sstride;
-#pragma unroll 1
-      for (int s = wc; s < kn / 64; s += kFewWarps) {  // 64 elements; this lane's 16-weight block: t
-        const uint4 x0 = lds128(x + 128u * s), x1 = lds128(x + 128u * s + 16u);
-        const uint32_t xv[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+      const uint32_t w = st + g * G::wstride + t * 16u, x = st + G::xoff + gx * xstride + t * 64u + (t >> 1) * 16u;
+      const uint32_t sc = st + G::soff + g * G::sstride + t * 2u;
+#pragma unroll 2
+      for (int s = wc; s < kn / 128; s += kFewWarps) {  // 128 elements; this lane's two blocks: 2 t, 2 t + 1
+        uint4 cw[4], xv[4];
+        uint32_t sw[4];
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          uint32_t a[2][8];
+        for (int i = 0; i < 4; ++i) {
+          cw[i] = lds128(w + 8u * i * G::wstride + 64u * s);
+          sw[i] = lds16(sc + 8u * i * G::sstride + 8u * s);
+        }
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t rr = 16u * m + 8u * i;
-            const uint2 c = lds64(w + rr * G::wstride + 32u * s);
-            const uint32_t b = e4m3_bcast_f16x2(lds32(sc + rr * G::sstride + 4u * s), static_cast<uint32_t>(t));
-            e2m1x8_to_f16x2(c.x, a[i][0], a[i][1], a[i][2], a[i][3]);
-            e2m1x8_to_f16x2(c.y, a[i][4], a[i][5], a[i][6], a[i][7]);
+        for (int i = 0; i < 4; ++i) xv[i] = lds128(x + 288u * s + 16u * i);
+        // 16 MMAs in four chains (row tile m, block h), which take turns
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // the lane's blocks: two code words a row each
+          uint32_t a[4][8];            // rows g, g + 8, g + 16, g + 24
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t b = __byte_perm(e4m3x2_to_f16x2(sw[i]), 0u, h ? 0x3232u : 0x1010u);
+            e2m1x8_to_f16x2(h ? cw[i].z : cw[i].x, a[i][0], a[i][1], a[i][2], a[i][3]);
+            e2m1x8_to_f16x2(h ? cw[i].w : cw[i].y, a[i][4], a[i][5], a[i][6], a[i][7]);
 #pragma unroll
             for (int q = 0; q < 8; ++q) a[i][q] = f16x2_mul(a[i][q], b);
           }
+          const uint32_t xw[8] = {xv[2 * h].x, xv[2 * h].y, xv[2 * h].z, xv[2 * h].w,
+                                  xv[2 * h + 1].x, xv[2 * h + 1].y, xv[2 * h + 1].z, xv[2 * h + 1].w};
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            mma_f16_16816(m == 0 ? lo : hi, a[0][2 * q], a[1][2 * q], a[0][2 * q + 1], a[1][2 * q + 1], xv[2 * q],
-                          xv[2 * q + 1]);
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+              mma_f16_16816(chain[h][m], a[2 * m][2 * q], a[2 * m + 1][2 * q], a[2 * m][2 * q + 1],
+                            a[2 * m + 1][2 * q + 1], xw[2 * q], xw[2 * q + 1]);
         }
       }
     } else {
       const uint32_t w = st + lane * G::wstride, x = st + G::xoff;
-#pragma unroll 1
+#pragma unroll 2
       for (int s = wc; s < kn / 4; s += kFewWarps) {
         const float4 a = as_float4(lds128(w + 16u * s));
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (j >= n) break;
-          const float4 b = as_float4(lds128(x + j * G::xstride + 16u * s));
+          const float4 b = as_float4(lds128(x + j * xstride + 16u * s));
           acc[j] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, acc[j]))));
         }
       }
@@ -660,7 +687,8 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int
     for (int j = 0; j < 8; ++j) mine[j * 33 + lane] = acc[j];
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) mine[(2 * t + (i & 1)) * 33 + 16 * (i >> 2) + 8 * ((i >> 1) & 1) + g] = acc[i];
+    for (int i = 0; i < 8; ++i) mine[(2 * t + (i & 1)) * 33 + 16 * (i >> 2) + 8 * ((i >> 1) & 1) + g] =
+        chain[0][i >> 2][i & 3] + chain[1][i >> 2][i & 3];
   }
   __syncwarp();
   if (lane == 0) mbar_arrive(out.full());
