@@ -138,6 +138,33 @@ __device__ __forceinline__ uint32_t ld_acquire_u32(const uint32_t* p) {
 __device__ __forceinline__ void red_release_u32(uint32_t* p, uint32_t v) {
   asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
+// mbar_wait with the wait left to the hardware (up to 20 us at a time): a warp that polls takes
+// issue slots and shared-memory cycles from the warps that work.
+__device__ __forceinline__ bool few_mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status,
+                                              uint32_t detail) {
+  auto test = [&]() -> bool {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+  };
+  if (test()) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!test()) {
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      *abort = 1;
+      record_status(status, kStatusTimeout, detail);
+      return false;
+    }
+  }
+  return true;
+}
 __device__ __forceinline__ void few_poll(const uint32_t* counter, uint32_t target, volatile int* abort,
                                          uint32_t* status, uint32_t detail) {
   if (ld_acquire_u32(counter) >= target) return;
@@ -481,7 +508,7 @@ __device__ __forceinline__ void few_produce(const FewSource<TA, FORMAT>& q, FewR
       for (int k0 = 0; k0 < K; k0 += kc) {
         const int kn = min(kc, K - k0);
         // (a wait that gave up: no copies; the arrivals go on so that nobody waits for them)
-        const bool ok = mbar_wait(ring.empty(), ring.phase ^ 1u, abort, p.status, 0xA00u + ring.stage);
+        const bool ok = few_mbar_wait(ring.empty(), ring.phase ^ 1u, abort, p.status, 0xA00u + ring.stage);
         if (__all_sync(0xffffffffu, ok)) {
           const uint32_t st = ring.addr();
           const int bytes = kn * G::act_size;
@@ -526,7 +553,7 @@ __device__ __forceinline__ void few_produce(const FewSource<TA, FORMAT>& q, FewR
 #pragma unroll 1
       for (int k0 = 0; k0 < K; k0 += kc) {
         const int kn = min(kc, K - k0), bytes = (FORMAT == FEW_NVFP4 ? kn / 2 : kn * G::act_size) - 16 * lane;
-        const bool ok = mbar_wait(ring.empty(), ring.phase ^ 1u, abort, p.status, 0xA00u + ring.stage);
+        const bool ok = few_mbar_wait(ring.empty(), ring.phase ^ 1u, abort, p.status, 0xA00u + ring.stage);
         if (__all_sync(0xffffffffu, ok)) {
           const uint32_t st = ring.addr() + 16 * lane + G::wstride * (pw - 1);
           const uint8_t* a0 = w0;
@@ -610,7 +637,7 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int
 #pragma unroll 1
   for (int k0 = 0; k0 < K; k0 += kc) {
     const int kn = min(kc, K - k0);
-    mbar_wait(ring.full(), ring.phase, abort, p.status, 0xC00u + ring.stage);
+    few_mbar_wait(ring.full(), ring.phase, abort, p.status, 0xC00u + ring.stage);
     __syncwarp();
     const uint32_t st = ring.addr();
     if constexpr (FORMAT == FEW_BF16) {
@@ -631,35 +658,35 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int
       const uint32_t sc = st + G::soff + g * G::sstride + t * 2u;
 #pragma unroll 2
       for (int s = wc; s < kn / 128; s += kFewWarps) {  // 128 elements; this lane's two blocks: 2 t, 2 t + 1
-        uint4 cw[4], xv[4];
+        uint4 cw[4];
         uint32_t sw[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           cw[i] = lds128(w + 8u * i * G::wstride + 64u * s);
           sw[i] = lds16(sc + 8u * i * G::sstride + 8u * s);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) xv[i] = lds128(x + 288u * s + 16u * i);
-        // 16 MMAs in four chains (row tile m, block h), which take turns
+        // 16 MMAs in four chains (block h, row tile m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // the lane's blocks: two code words a row each
-          uint32_t a[4][8];            // rows g, g + 8, g + 16, g + 24
+          const uint4 x0 = lds128(x + 288u * s + 32u * h), x1 = lds128(x + 288u * s + 32u * h + 16u);
+          const uint32_t xw[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t b = __byte_perm(e4m3x2_to_f16x2(sw[i]), 0u, h ? 0x3232u : 0x1010u);
-            e2m1x8_to_f16x2(h ? cw[i].z : cw[i].x, a[i][0], a[i][1], a[i][2], a[i][3]);
-            e2m1x8_to_f16x2(h ? cw[i].w : cw[i].y, a[i][4], a[i][5], a[i][6], a[i][7]);
+          for (int m = 0; m < 2; ++m) {
+            uint32_t a[2][8];            // rows g and g + 8 of the tile
 #pragma unroll
-            for (int q = 0; q < 8; ++q) a[i][q] = f16x2_mul(a[i][q], b);
+            for (int j = 0; j < 2; ++j) {
+              const int i = 2 * m + j;
+              const uint32_t b = __byte_perm(e4m3x2_to_f16x2(sw[i]), 0u, h ? 0x3232u : 0x1010u);
+              e2m1x8_to_f16x2(h ? cw[i].z : cw[i].x, a[j][0], a[j][1], a[j][2], a[j][3]);
+              e2m1x8_to_f16x2(h ? cw[i].w : cw[i].y, a[j][4], a[j][5], a[j][6], a[j][7]);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) a[j][q] = f16x2_mul(a[j][q], b);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              mma_f16_16816(chain[h][m], a[0][2 * q], a[1][2 * q], a[0][2 * q + 1], a[1][2 * q + 1], xw[2 * q],
+                            xw[2 * q + 1]);
           }
-          const uint32_t xw[8] = {xv[2 * h].x, xv[2 * h].y, xv[2 * h].z, xv[2 * h].w,
-                                  xv[2 * h + 1].x, xv[2 * h + 1].y, xv[2 * h + 1].z, xv[2 * h + 1].w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-              mma_f16_16816(chain[h][m], a[2 * m][2 * q], a[2 * m + 1][2 * q], a[2 * m][2 * q + 1],
-                            a[2 * m + 1][2 * q + 1], xw[2 * q], xw[2 * q + 1]);
         }
       }
     } else {
@@ -679,7 +706,7 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int
     if (lane == 0) mbar_arrive(ring.empty());
     ring.next();
   }
-  mbar_wait(out.free(), out.phase ^ 1u, abort, p.status, 0xD00u);
+  few_mbar_wait(out.free(), out.phase ^ 1u, abort, p.status, 0xD00u);
   __syncwarp();
   float* mine = out.red() + wc * 8 * 33;
   if constexpr (FORMAT == FEW_F32) {
@@ -831,7 +858,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_cons
     };
     // the sums of a chunk: store(chunk, token, lane's row, sum) on warp token % kFewStore
     auto chunk = [&](const FewChunks& c, int n, auto store) {
-      mbar_wait(red.full(), red.phase, abort, p.status, 0xE00u);
+      few_mbar_wait(red.full(), red.phase, abort, p.status, 0xE00u);
       __syncwarp();
 #pragma unroll 1
       for (int j = ws; j < n; j += kFewStore) store(c, j, few_sum(red.red(), j, lane));
