@@ -68,11 +68,14 @@ struct Gemm2Shape {
 // groups of four (one warp per TMEM lane quadrant each) taking alternate token chunks
 constexpr int kPairThreads = 320;
 
-template <typename TOut, int EPI, int MT>
+template <typename TOut, int EPI, int MT, typename TIn = __nv_bfloat16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_umma_gemm_2sm(const __grid_constant__ TmaMaps maps, const GemmArgs p) {
   using S = Gemm2Shape<EPI, MT>;
-  using TIn = __nv_bfloat16;
+  constexpr bool kInt8 = sizeof(TIn) == 1;
+  static_assert(!kInt8 || EPI != EPI_SWIGLU, "int8 operands: dense products");
+  // the M = 256 MMA's N granularity
+  constexpr int kNStep = kInt8 ? 32 : 16;
   constexpr bool kDual = S::kDual;
   constexpr int kStages = S::kStages;
 
@@ -193,12 +196,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         if (t < 0) break;
         int g, m0, row0, n;
-        gemm_tile(p, t, S::kBN, g, m0, row0, n);
-        // N = n rounded up to 16 (the M = 256 MMA's N granularity); each CTA stages N / 2
+        gemm_tile(p, t, tile_tokens(p, S::kBN), g, m0, row0, n);
+        // N = n rounded up to 16 (int8: 32), the M = 256 MMA's N granularity; each CTA stages N / 2
         // token rows, a multiple of 8, loaded as 16-row boxes: the last box may carry 8 rows
         // past the half (the partner's first rows, or zero fill past the tensor), which
         // still lie inside the stage's 128-row B area and count in the expected bytes
-        const int N = (n + 15) & ~15;
+        const int N = (n + kNStep - 1) & -kNStep;
         const int half = N >> 1;             // token rows the MMA reads from this CTA
         const int nb16 = (half + 15) >> 4;   // 1..8 boxes of 16 rows
         const uint32_t bytes_pair = 2u * (S::kABytes * MT + static_cast<uint32_t>(nb16) * 2048u);
@@ -213,7 +216,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           const uint32_t fb = mapa_shared(full_bar(stage), 0);
           if (leader) mbar_arrive_expect_tx(full_bar(stage), bytes_pair);
           const uint32_t sA = smem_u32(smem + stage * S::kStageBytes);
-          const int kc = kb * 64;
+          const int kc = kb * static_cast<int>(128 / sizeof(TIn));
           tma_load_2d_pair(sA, &maps.a, fb, kc, a_row);
           if (kDual) tma_load_2d_pair(sA + S::kABytes, &maps.a2, fb, kc, a2_row);
           const uint32_t sB = sA + S::kABytes * MT;
@@ -258,9 +261,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         release_tile(i);
         if (t < 0) break;
         int g, m0, row0, n;
-        gemm_tile(p, t, S::kBN, g, m0, row0, n);
-        const uint32_t N = static_cast<uint32_t>((n + 15) & ~15);
-        const uint32_t idesc = idesc_f32acc(1u, 256u, N);
+        gemm_tile(p, t, tile_tokens(p, S::kBN), g, m0, row0, n);
+        const uint32_t N = static_cast<uint32_t>((n + kNStep - 1) & -kNStep);
+        const uint32_t idesc = kInt8 ? idesc_i8(256u, N) : idesc_f32acc(1u, 256u, N);
         if (!mbar_wait<true>(acce_bar(acc), acc_phase ^ 1u, abort_flag, p.status, 0x600u + acc)) {
           ok = false;
           break;
@@ -279,8 +282,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           for (int kk = 0; kk < 4; ++kk) {
             const uint32_t accum = (kb > 0 || kk > 0) ? 1u : 0u;
             const uint64_t db = sdesc_k_sw128(sB + 32u * kk);
-            umma_pair_bf16(d, sdesc_k_sw128(sA + 32u * kk), db, idesc, accum);
-            if (kDual) umma_pair_bf16(d + 256u, sdesc_k_sw128(sA + S::kABytes + 32u * kk), db, idesc, accum);
+            if constexpr (kInt8) {
+              umma_pair_i8(d, sdesc_k_sw128(sA + 32u * kk), db, idesc, accum);
+              if (kDual) umma_pair_i8(d + 256u, sdesc_k_sw128(sA + S::kABytes + 32u * kk), db, idesc, accum);
+            } else {
+              umma_pair_bf16(d, sdesc_k_sw128(sA + 32u * kk), db, idesc, accum);
+              if (kDual) umma_pair_bf16(d + 256u, sdesc_k_sw128(sA + S::kABytes + 32u * kk), db, idesc, accum);
+            }
           }
           issued_any = true;
           tc_commit_pair(empty_bar(stage), 0x3);
@@ -317,7 +325,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     int sbuf = 0;
     auto emit = [&](const float (&val)[32], int c, int col0, int row0, int n, bool f_ok, int f) {
       TOut* out = reinterpret_cast<TOut*>(p.out);
-      if constexpr (kTmaStore) {
+      if (kTmaStore && !(kInt8 && p.plain_store)) {
         if (elected) bulk_wait_group_read<1>();  // the buffer's previous store has read it
         epilogue_group_bar_sync(grp);
         __nv_bfloat16* buf = reinterpret_cast<__nv_bfloat16*>(grp_stage + sbuf * S::kOutBufBytes);
@@ -350,7 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (lane == 0) release_tile(i);
       if (t < 0) break;
       int g, m0, row0, n;
-      gemm_tile(p, t, S::kBN, g, m0, row0, n);
+      gemm_tile(p, t, tile_tokens(p, S::kBN), g, m0, row0, n);
       const bool ready = mbar_wait<true>(accf_bar(acc), acc_phase, abort_flag, p.status, 0x800u + acc);
       if (!__all_sync(0xffffffffu, ready)) break;
       tc_fence_after();
@@ -395,15 +403,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           tmem_ld_wait();
         }
       } else {
-        float gain1[MT];
+        float gain1[MT], wscale[MT];
         bool fok[MT];
 #pragma unroll
         for (int h = 0; h < MT; ++h) {
           const int f = col_cta + h * 256 + fl;
           fok[h] = f < p.m_valid;
           gain1[h] = 1.0f;
+          using TGain = typename std::conditional<kInt8, TOut, TIn>::type;
           if (EPI == EPI_STORE_SS && p.ss_gain != nullptr && fok[h])
-            gain1[h] = 1.0f + to_f32(reinterpret_cast<const TIn*>(p.ss_gain)[g * p.ss_gain_group_stride + f]);
+            gain1[h] = 1.0f + to_f32(reinterpret_cast<const TGain*>(p.ss_gain)[g * p.ss_gain_group_stride + f]);
+          wscale[h] = 1.0f;
+          if (kInt8) wscale[h] = fok[h] ? p.w_scale[f] : 0.0f;
         }
         constexpr int kItems = MT * (S::kBN / 64);
         const int valid = MT * m;  // item j: chunk grp + 2 * (j / MT), accumulator half j % MT
@@ -416,6 +427,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           float yv[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) yv[i] = __uint_as_float(v[i]);
+          if constexpr (kInt8) {
+            const float xs = chunk_scale(p, row0, c, n, lane);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              yv[i] = acc_value<TIn>(v[i], __shfl_sync(0xffffffffu, xs, i) * wscale[h]);
+          }
           emit(yv, c, col_cta + h * 256, row0, n, fok[h], col_cta + h * 256 + fl);
           if constexpr (EPI == EPI_STORE_SS) {
 #pragma unroll

@@ -232,13 +232,13 @@ bool make_u8_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, i
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Output map for TMA stores: rows x cols bf16 row-major, boxes of 16 rows x 128 columns,
-// no swizzle (the epilogue stages tiles row-major in shared memory).
-bool make_out_map(CUtensorMap* m, void* base, int64_t rows, int64_t cols) {
+// Output map for TMA stores: rows x cols bf16, rows ld elements apart (0: cols), boxes of 16 rows x
+// 128 columns, no swizzle (the epilogue stages tiles row-major in shared memory).
+bool make_out_map(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int64_t ld = 0) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld > 0 ? ld : cols) * 2};
   cuuint32_t box[2] = {128u, 16u};
   cuuint32_t estr[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -361,9 +361,9 @@ bool make_w4a4_maps(W4A4Maps* m, const muse_nvfp4_weight* w, const muse_nvfp4_we
          make_u8_map(&m->sfb, scales, R, K / 16, 16, bn, false);
 }
 
-template <typename TOut, int EPI, int MT>
+template <typename TOut, int EPI, int MT, typename TIn = __nv_bfloat16>
 cudaError_t launch_gemm_2sm(const TmaMaps& maps, const GemmArgs& args, int pairs, cudaStream_t st) {
-  auto kern = k_umma_gemm_2sm<TOut, EPI, MT>;
+  auto kern = k_umma_gemm_2sm<TOut, EPI, MT, TIn>;
   const size_t smem = Gemm2Shape<EPI, MT>::kSmemBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -1270,9 +1270,84 @@ muse_status quantize_int8(const void* src, int32_t dtype, int64_t rows, int64_t 
   return MUSE_OK;
 }
 
+// How an int8 product of many rows is tiled: on CTA pairs (256 features x tokens) or single CTAs
+// (128 x tokens). A tile's time goes with the operand bytes its SM fetches per k-block (128 weight
+// rows and all, on a pair half, of its token rows); the plan with the smallest product of waves and
+// bytes wins, the larger tile among equals.
+struct Int8Plan {
+  bool pair;
+  int tokens;
+};
+Int8Plan int8_plan(int64_t T, int64_t N) {
+  const int nsm = sm_count();
+  Int8Plan best{true, 256};
+  int64_t best_cost = INT64_MAX;
+  for (int tokens = 256; tokens >= 32; tokens -= 32)
+    for (int pair = 1; pair >= 0; --pair) {
+      const int64_t tiles = cdiv(T, tokens) * cdiv(N, pair ? 256 : 128), slots = pair ? nsm / 2 : nsm;
+      const int64_t cost = cdiv(tiles, slots) * (128 + (pair ? tokens / 2 : tokens));
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = {pair != 0, tokens};
+      }
+    }
+  return best;
+}
+
+template <typename TOut, int EPI = EPI_STORE>
+muse_status int8_gemm(const void* xc, const float* xs, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
+                      void* out, int64_t ldo, uint32_t* status, cudaStream_t st, DenseSS sq = DenseSS{}) {
+  if (encode_fn() == nullptr) return MUSE_ERR_CUDA;
+  const Int8Plan plan = int8_plan(T, N);
+  TmaMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  if (!make_u8_map(&maps.a, w.codes, N, K, 128, 128, true) || !make_u8_map(&maps.a2, w.codes, N, K, 128, 128, true))
+    return MUSE_ERR_CUDA;
+  for (int i = 0; i < 5; ++i)
+    if (!make_u8_map(&maps.b[i], xc, T, K, 128, 16 << i, true)) return MUSE_ERR_CUDA;
+  GemmArgs g = base_args(status);
+  const int nsm = sm_count();
+  g.m_valid = static_cast<int>(N);
+  g.T = static_cast<int>(T);
+  g.k_blocks = static_cast<int>(cdiv(K, 128));
+  g.out = out;
+  g.ld_out = ldo;
+  g.x_scale = xs;
+  g.w_scale = w.scales;
+  g.ss = sq.ss;
+  g.ss_ld = sq.ld;
+  g.ss_gain = sq.gain;
+  // token chunks as equal as possible
+  g.bn = static_cast<int>(align_up(static_cast<size_t>(cdiv(T, cdiv(T, plan.tokens))), 32));
+  g.m_step = plan.pair ? 256 : 128;
+  g.m_tiles = static_cast<int>(cdiv(N, g.m_step));
+  g.num_tiles = static_cast<int>(g.m_tiles * cdiv(T, g.bn));
+  if (plan.pair) {
+    // (bf16 tiles leave by TMA where the output's rows start on 16 bytes)
+    if constexpr (sizeof(TOut) == 2) {
+      g.plain_store = !aligned16(out) || ldo % 8 != 0;
+      if (!g.plain_store && !make_out_map(&maps.out, out, T, N, ldo)) return MUSE_ERR_CUDA;
+    }
+    if (N >= T)
+      g.m_group = static_cast<int>(std::max<int64_t>(1, (int64_t(32) << 20) / (g.m_step * K)));
+    MUSE_CK((launch_gemm_2sm<TOut, EPI, 1, int8_t>(maps, g, std::min(g.num_tiles, nsm / 2), st)));
+    return MUSE_OK;
+  }
+  const int grid = std::min(g.num_tiles, nsm);
+  if (g.bn <= 32) {
+    MUSE_CK((launch_gemm<int8_t, TOut, 32, EPI, 1>(maps, g, grid, st)));
+  } else if (g.bn <= 128) {
+    MUSE_CK((launch_gemm<int8_t, TOut, 128, EPI, 1>(maps, g, grid, st)));
+  } else {
+    MUSE_CK((launch_gemm<int8_t, TOut, 256, EPI, 1>(maps, g, grid, st)));
+  }
+  return MUSE_OK;
+}
+
 template <typename TOut>
 muse_status int8_product(const void* xc, const float* xs, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
                          void* out, int64_t ldo, uint32_t* status, cudaStream_t st) {
+  if (T > 64) return int8_gemm<TOut>(xc, xs, T, K, w, N, out, ldo, status, st);
   const dim3 grid(static_cast<unsigned>(cdiv(N, 8)), static_cast<unsigned>(std::min<int64_t>(cdiv(T, 8), 65535)));
   k_int8_matmul<TOut><<<grid, 256, 0, st>>>(static_cast<const int8_t*>(xc), xs, static_cast<int>(T),
                                             static_cast<int>(K), static_cast<const int8_t*>(w.codes), w.scales,
