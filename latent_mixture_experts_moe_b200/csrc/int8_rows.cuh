@@ -22,38 +22,126 @@ namespace muse {
 
 constexpr float kInt8ScaleMin = 1.17549435e-38f;  // 2^-126
 
-// amax (NaN or infinity: none) -> the row's scale
-__device__ __forceinline__ float int8_scale(float amax) {
-  return amax <= 3.402823466e38f ? fmaxf(amax / 127.0f, kInt8ScaleMin) : __int_as_float(0x7fc00000);
+// The row's scale from the bits of its largest magnitude (as integers they order like the
+// magnitudes, infinity and then NaN last).
+__device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
+  return amax_bits < 0x7f800000u ? fmaxf(__uint_as_float(amax_bits) / 127.0f, kInt8ScaleMin)
+                                 : __int_as_float(0x7fc00000);
 }
-__device__ __forceinline__ int int8_code(float v, float scale) {
-  return scale == scale ? __float2int_rn(v / scale) : 0;
+__device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+__device__ __forceinline__ uint32_t int8_pack(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040u), __byte_perm(c, d, 0x0040u), 0x5410u);
 }
-// max(a, |v|) that keeps a NaN
-__device__ __forceinline__ float amax_nan(float a, float v) {
-  v = fabsf(v);
-  return (a >= v || a != a) ? a : v;  // v NaN: the comparison fails and v is kept
+// (kept out of line: rare, and its registers would cost occupancy)
+__device__ __noinline__ uint32_t int8_divide4(float a, float b, float c, float d, float scale) {
+  return int8_pack(__float2int_rn(a / scale), __float2int_rn(b / scale), __float2int_rn(c / scale),
+                   __float2int_rn(d / scale));
+}
+// Eight codes: v / scale rounded to nearest, ties to even; inv = 1 / scale. v * inv is within 3
+// units in the last place of the quotient (at most 127: within 3 * 2^-17), so both round to the
+// same integer unless the product is that near to a half; only then the eight divisions are
+// done. Rounding by adding 1.5 * 2^23 leaves the integer in the sum's low bits.
+__device__ __forceinline__ uint2 int8_codes8(const float (&v)[8], float scale, float inv) {
+  constexpr float kRound = 12582912.0f;
+  uint32_t q[8];
+  float off = 0.0f;  // largest distance from an integer
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float r = v[i] * inv, t = r + kRound;
+    q[i] = __float_as_uint(t);
+    off = fmaxf(off, fabsf(r - (t - kRound)));
+  }
+  if (scale != scale) return make_uint2(0u, 0u);
+  if (off > 0.4999f)
+    return make_uint2(int8_divide4(v[0], v[1], v[2], v[3], scale), int8_divide4(v[4], v[5], v[6], v[7], scale));
+  return make_uint2(int8_pack(q[0], q[1], q[2], q[3]), int8_pack(q[4], q[5], q[6], q[7]));
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_quant_rows_int8(const T* __restrict__ src, int64_t ld, int rows, int K,
-                                                         int8_t* __restrict__ codes, float* __restrict__ scales) {
-  __shared__ float part[32];
-  for (int r = blockIdx.x; r < rows; r += gridDim.x) {
-    const T* x = src + static_cast<int64_t>(r) * ld;
-    float a = 0.0f;
-    for (int i = threadIdx.x; i < K; i += blockDim.x) a = amax_nan(a, to_f32(x[i]));
+// eight consecutive values; ALIGNED: from a 16-byte boundary
+template <typename T, bool ALIGNED>
+struct Int8Load {
+  T raw[8];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (ALIGNED) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) a = amax_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = a;
-    __syncthreads();
-    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) a = amax_nan(a, part[w]);
-    const float s = int8_scale(a);
-    for (int i = threadIdx.x; i < K; i += blockDim.x)
-      codes[static_cast<int64_t>(r) * K + i] = static_cast<int8_t>(int8_code(to_f32(x[i]), s));
-    if (threadIdx.x == 0) scales[r] = s;
+      for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+        reinterpret_cast<uint4*>(raw)[i] = reinterpret_cast<const uint4*>(p)[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) raw[i] = p[i];
+    }
   }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f32(raw[i]);
+  }
+};
+
+// TPR threads per row (32, 128 or 256), which hold up to 32 values each, so that a row of up to 32 TPR
+// values is read once, all its loads in flight together; longer rows are read again for the
+// codes (from L2). Bound by reading the rows and writing the codes; five blocks an SM keep
+// enough loads in flight (8192 x 8192 bf16: 83 us with two).
+template <typename T, int TPR, bool ALIGNED>
+__global__ void __launch_bounds__(256, 5) k_quant_rows_int8(const T* __restrict__ src, int64_t ld, int rows, int K,
+                                                         int8_t* __restrict__ codes, float* __restrict__ scales) {
+  constexpr int kVecs = 4;
+  __shared__ uint32_t part[8];
+  const int sub = threadIdx.x % TPR;
+  const int r = blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
+  if (r >= rows) return;  // (all threads of the row)
+  const T* x = src + static_cast<int64_t>(r) * ld;
+  int8_t* out = codes + static_cast<int64_t>(r) * K;
+  Int8Load<T, ALIGNED> hold[kVecs];
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int k = (i * TPR + sub) * 8;
+    if (k < K) hold[i].load(x + k);
+  }
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    if ((i * TPR + sub) * 8 < K) {
+      float v[8];
+      hold[i].get(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = max(amax, magnitude_bits(v[j]));
+    }
+  }
+  for (int k = (kVecs * TPR + sub) * 8; k < K; k += TPR * 8) {
+    Int8Load<T, ALIGNED> more;
+    more.load(x + k);
+    float v[8];
+    more.get(v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = max(amax, magnitude_bits(v[j]));
+  }
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  if constexpr (TPR > 32) {
+    const int first = threadIdx.x / TPR * (TPR / 32);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x) / TPR), "n"(TPR) : "memory");
+#pragma unroll
+    for (int w = 0; w < TPR / 32; ++w) amax = max(amax, part[first + w]);
+  }
+  const float s = int8_scale(amax), inv = 1.0f / s;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int k = (i * TPR + sub) * 8;
+    if (k < K) {
+      float v[8];
+      hold[i].get(v);
+      *reinterpret_cast<uint2*>(out + k) = int8_codes8(v, s, inv);
+    }
+  }
+  for (int k = (kVecs * TPR + sub) * 8; k < K; k += TPR * 8) {
+    Int8Load<T, ALIGNED> more;
+    more.load(x + k);
+    float v[8];
+    more.get(v);
+    *reinterpret_cast<uint2*>(out + k) = int8_codes8(v, s, inv);
+  }
+  if (sub == 0) scales[r] = s;
 }
 
 // A warp per output channel and 8 rows of x; four products per instruction.

@@ -1257,38 +1257,50 @@ bool aligned_to(const void* p, size_t a) { return p != nullptr && reinterpret_ca
 size_t dtype_size(int32_t dtype) { return dtype == MUSE_BF16 ? 2 : 4; }
 bool valid_dtype(int32_t dtype) { return dtype == MUSE_F32 || dtype == MUSE_BF16; }
 
-muse_status quantize_int8(const void* src, int32_t dtype, int64_t rows, int64_t K, int64_t ld, void* codes,
-                          float* scales, cudaStream_t st) {
-  const int grid = static_cast<int>(std::min<int64_t>(rows, 16 * sm_count()));
-  if (dtype == MUSE_BF16)
-    k_quant_rows_int8<<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(src), ld, static_cast<int>(rows),
-                                            static_cast<int>(K), static_cast<int8_t*>(codes), scales);
-  else
-    k_quant_rows_int8<<<grid, 256, 0, st>>>(static_cast<const float*>(src), ld, static_cast<int>(rows),
-                                            static_cast<int>(K), static_cast<int8_t*>(codes), scales);
+template <typename T>
+muse_status quantize_int8_t(const T* src, int64_t rows, int64_t K, int64_t ld, int8_t* codes, float* scales,
+                            cudaStream_t st) {
+  const bool aligned = aligned16(src) && (rows == 1 || ld * static_cast<int64_t>(sizeof(T)) % 16 == 0);
+  const int n = static_cast<int>(rows), k = static_cast<int>(K);
+  // as many threads as hold the row at 32 values each, at most a block
+  const int tpr = K <= 32 * 32 ? 32 : K <= 32 * 128 ? 128 : 256;
+  auto kern = tpr == 32    ? (aligned ? k_quant_rows_int8<T, 32, true> : k_quant_rows_int8<T, 32, false>)
+              : tpr == 128 ? (aligned ? k_quant_rows_int8<T, 128, true> : k_quant_rows_int8<T, 128, false>)
+                           : (aligned ? k_quant_rows_int8<T, 256, true> : k_quant_rows_int8<T, 256, false>);
+  kern<<<static_cast<unsigned>(cdiv(rows, 256 / tpr)), 256, 0, st>>>(src, ld, n, k, codes, scales);
   MUSE_CK(cudaGetLastError());
   return MUSE_OK;
 }
 
-// How an int8 product of many rows is tiled: on CTA pairs (256 features x tokens) or single CTAs
-// (128 x tokens). A tile's time goes with the operand bytes its SM fetches per k-block (128 weight
-// rows and all, on a pair half, of its token rows); the plan with the smallest product of waves and
-// bytes wins, the larger tile among equals.
+muse_status quantize_int8(const void* src, int32_t dtype, int64_t rows, int64_t K, int64_t ld, void* codes,
+                          float* scales, cudaStream_t st) {
+  int8_t* c = static_cast<int8_t*>(codes);
+  return dtype == MUSE_BF16 ? quantize_int8_t(static_cast<const __nv_bfloat16*>(src), rows, K, ld, c, scales, st)
+                            : quantize_int8_t(static_cast<const float*>(src), rows, K, ld, c, scales, st);
+}
+
+// How an int8 product of many rows is tiled: on CTA pairs (256 mt features x tokens) or single CTAs
+// (128 x tokens). A tile's clocks per 128-byte k-block are those of its MMAs (2 per token and 256
+// features) or of fetching its operands (128 mt weight rows and all, on a pair half, of its token
+// rows, at the ~48 bytes a clock an SM gets from L2), whichever is more; with two accumulators (mt =
+// 2) the epilogue, ~20 clocks a token, is not hidden behind the next tile. The plan with the least
+// sum over its waves wins.
 struct Int8Plan {
   bool pair;
-  int tokens;
+  int mt, tokens;
 };
-Int8Plan int8_plan(int64_t T, int64_t N) {
+Int8Plan int8_plan(int64_t T, int64_t N, int64_t K) {
   const int nsm = sm_count();
-  Int8Plan best{true, 256};
+  Int8Plan best{true, 1, 256};
   int64_t best_cost = INT64_MAX;
   for (int tokens = 256; tokens >= 32; tokens -= 32)
-    for (int pair = 1; pair >= 0; --pair) {
-      const int64_t tiles = cdiv(T, tokens) * cdiv(N, pair ? 256 : 128), slots = pair ? nsm / 2 : nsm;
-      const int64_t cost = cdiv(tiles, slots) * (128 + (pair ? tokens / 2 : tokens));
+    for (int mt = 2; mt >= 0; --mt) {  // 0: a single CTA
+      const int64_t tiles = cdiv(T, tokens) * cdiv(N, mt ? 256 * mt : 128), slots = mt ? nsm / 2 : nsm;
+      const int64_t mma = 2 * tokens * std::max(mt, 1), load = (128 * std::max(mt, 1) + (mt ? tokens / 2 : tokens)) * 8 / 3;
+      const int64_t cost = cdiv(tiles, slots) * (cdiv(K, 128) * std::max(mma, load) + (mt == 2 ? 20 * tokens : 0) + 1500);
       if (cost < best_cost) {
         best_cost = cost;
-        best = {pair != 0, tokens};
+        best = {mt != 0, std::max(mt, 1), tokens};
       }
     }
   return best;
@@ -1298,7 +1310,7 @@ template <typename TOut, int EPI = EPI_STORE>
 muse_status int8_gemm(const void* xc, const float* xs, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
                       void* out, int64_t ldo, uint32_t* status, cudaStream_t st, DenseSS sq = DenseSS{}) {
   if (encode_fn() == nullptr) return MUSE_ERR_CUDA;
-  const Int8Plan plan = int8_plan(T, N);
+  const Int8Plan plan = int8_plan(T, N, K);
   TmaMaps maps;
   std::memset(&maps, 0, sizeof(maps));
   if (!make_u8_map(&maps.a, w.codes, N, K, 128, 128, true) || !make_u8_map(&maps.a2, w.codes, N, K, 128, 128, true))
@@ -1319,7 +1331,7 @@ muse_status int8_gemm(const void* xc, const float* xs, int64_t T, int64_t K, con
   g.ss_gain = sq.gain;
   // token chunks as equal as possible
   g.bn = static_cast<int>(align_up(static_cast<size_t>(cdiv(T, cdiv(T, plan.tokens))), 32));
-  g.m_step = plan.pair ? 256 : 128;
+  g.m_step = plan.pair ? 256 * plan.mt : 128;
   g.m_tiles = static_cast<int>(cdiv(N, g.m_step));
   g.num_tiles = static_cast<int>(g.m_tiles * cdiv(T, g.bn));
   if (plan.pair) {
@@ -1330,7 +1342,9 @@ muse_status int8_gemm(const void* xc, const float* xs, int64_t T, int64_t K, con
     }
     if (N >= T)
       g.m_group = static_cast<int>(std::max<int64_t>(1, (int64_t(32) << 20) / (g.m_step * K)));
-    MUSE_CK((launch_gemm_2sm<TOut, EPI, 1, int8_t>(maps, g, std::min(g.num_tiles, nsm / 2), st)));
+    const int pairs = std::min(g.num_tiles, nsm / 2);
+    if (plan.mt == 2) MUSE_CK((launch_gemm_2sm<TOut, EPI, 2, int8_t>(maps, g, pairs, st)));
+    else MUSE_CK((launch_gemm_2sm<TOut, EPI, 1, int8_t>(maps, g, pairs, st)));
     return MUSE_OK;
   }
   const int grid = std::min(g.num_tiles, nsm);
