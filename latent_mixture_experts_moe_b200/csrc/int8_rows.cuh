@@ -15,6 +15,7 @@
 #include <cstdint>
 #include <cuda_bf16.h>
 
+#include "few_tokens.cuh"
 #include "gemm_umma.cuh"
 #include "route_kernels.cuh"
 
@@ -144,32 +145,219 @@ __global__ void __launch_bounds__(256, 5) k_quant_rows_int8(const T* __restrict_
   if (sub == 0) scales[r] = s;
 }
 
-// A warp per output channel and 8 rows of x; four products per instruction.
-template <typename TOut>
-__global__ void __launch_bounds__(256) k_int8_matmul(const int8_t* __restrict__ x, const float* __restrict__ sx, int T,
-                                                     int K, const int8_t* __restrict__ w,
-                                                     const float* __restrict__ sw, int N, TOut* __restrict__ out,
-                                                     int64_t ldo) {
-  const int lane = threadIdx.x & 31;
-  const int n = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (n >= N) return;  // warp-uniform
-  for (int t0 = blockIdx.y * 8; t0 < T; t0 += 8 * gridDim.y) {
-    int acc[8] = {};
-    for (int k0 = lane * 16; k0 < K; k0 += 512) {
-      const int4 a = *reinterpret_cast<const int4*>(w + static_cast<int64_t>(n) * K + k0);
+// The product of at most 64 rows: weight rows streamed once, as in few_tokens.cuh. The channels
+// are divided evenly over the CTAs (one per SM). Four producer warps fill a ring of stages, R
+// weight rows and the activation rows x KC bytes of K, by 16-byte asynchronous copies. Eight
+// product warps (R / 32 groups of 32 rows, each splitting K) run m16n8k32 integer MMAs: weight
+// rows as A, eight tokens as B's columns; lane (g, t) reads 16 consecutive bytes of rows g and
+// g + 8 and of token g, and K's order is that of these bytes in both operands. Past K the
+// activations are zeros. The warps' sums are added through shared memory, 16 tokens at a time.
+// FUSED (at most 8 float rows): every CTA quantises the rows itself while its ring fills, one
+// launch less and no round trip through memory.
+// Bound by reading the weights; with 64 rows by the activations every SM fetches too (R = 64
+// halves those), and 4.3 GOP at the warp-level integer MMA's 1.1 POPS (measured) are 3.8 us.
+template <int NT, bool FUSED>
+struct Int8Stream {
+  static constexpr int R = NT >= 4 ? 64 : 32;                      // weight rows of a stage
+  static constexpr int KC = NT >= 4 ? 256 : NT == 2 ? 512 : 1024;  // bytes of K of a stage
+  static constexpr int kGroups = R / 32, kSplit = 8 / kGroups;     // row groups; product warps per group
+  static constexpr uint32_t kStride = KC + 64;                     // see FewGeo on bank conflicts
+  static constexpr uint32_t kXOff = R * kStride;
+  static constexpr uint32_t stage_bytes(int T) { return (kXOff + (FUSED ? 0 : T) * kStride + 127) / 128 * 128; }
+  static constexpr uint32_t kRedBytes = 8u * 16u * 33u * 4u;
+  static constexpr int kThreads = 32 * 12;
+  // fused: distance of the quantised rows
+  __host__ __device__ static constexpr uint32_t xstride(int K) { return static_cast<uint32_t>((K + 127) / 128 * 128 + 64); }
+};
+constexpr int kInt8FusedBytes = 72 * 1024;  // quantised rows a fused call may hold
+
+struct Int8StreamArgs {
+  const void* x;            // codes [T, K], or (fused) float rows ldx apart
+  int64_t ldx;
+  const float* x_scale;     // of the codes
+  const int8_t* w;
+  const float* w_scale;
+  void* out;
+  int64_t ldo;
+  int T, K, N, stages;
+  uint32_t* status;
+};
+
+__device__ __forceinline__ void mma_s8_16832(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 16 bytes, or zeros
+__device__ __forceinline__ void cp_async16_or_zero(bool copy, uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(copy ? 16u : 0u) : "memory");
+}
+
+template <int NT, bool FUSED, typename TX, typename TOut>
+__global__ void __launch_bounds__(Int8Stream<NT, FUSED>::kThreads, 1) k_int8_stream(const Int8StreamArgs p) {
+  using S = Int8Stream<NT, FUSED>;
+  extern __shared__ __align__(128) uint8_t smem[];  // partial sums, quantised rows (fused), the ring
+  __shared__ __align__(8) uint64_t bars[2 * kFewMaxStages];
+  __shared__ uint32_t part[8];
+  __shared__ float xs[8 * NT];
+  __shared__ int abort_flag;
+  volatile int* abort = &abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int T = p.T, K = p.K;
+  const uint32_t xq = smem_u32(smem) + S::kRedBytes;
+  FewRing ring{smem_u32(bars), xq + (FUSED ? (T * S::xstride(K) + 127) / 128 * 128 : 0u), p.stages, 0, 0u,
+               S::stage_bytes(T)};
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(smem_u32(bars + i), 128);
+      mbar_init(smem_u32(bars + kFewMaxStages + i), 8);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  FewChunks c(p.N, p.N, S::R);
+
+  if (warp < 4) {
+    // ------------------------------------------------------------------------- producers
+    constexpr int kPer = S::KC / 16, kStep = 128 / kPer;  // 16-byte pieces of a row; rows per pass
+    const int row = threadIdx.x / kPer, o = threadIdx.x % kPer * 16;
+    const int8_t* xc = static_cast<const int8_t*>(p.x) + static_cast<int64_t>(row) * (FUSED ? 0 : K) + o;
+    const int64_t step = static_cast<int64_t>(kStep) * K;
+    for (; !c.done(); c.next()) {
+      const int8_t* wc = p.w + static_cast<int64_t>(c.f + row) * K + o;
+#pragma unroll 1
+      for (int k0 = 0; k0 < K; k0 += S::KC) {
+        const bool ok = few_mbar_wait(ring.empty(), ring.phase ^ 1u, abort, p.status, 0xA10u + ring.stage);
+        if (__all_sync(0xffffffffu, ok)) {
+          const uint32_t st = ring.addr() + row * S::kStride + o;
+          const int8_t* a = wc + k0;
+          const bool in = k0 + o < K;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (t0 + j < T) {
-          const int4 b = *reinterpret_cast<const int4*>(x + static_cast<int64_t>(t0 + j) * K + k0);
-          acc[j] = __dp4a(a.x, b.x, __dp4a(a.y, b.y, __dp4a(a.z, b.z, __dp4a(a.w, b.w, acc[j]))));
+          for (int r = 0; r < S::R; r += kStep) {
+            cp_async16_if(in && r + row < c.len, st + r * S::kStride, a);
+            a += step;
+          }
+          if constexpr (!FUSED) {
+            // (a unit of K is 64 bytes: zeros up to its end)
+            const int8_t* b = xc + k0;
+            const bool fill = k0 + o < ((K + 63) & ~63);
+#pragma unroll 4
+            for (int r = 0; r < T; r += kStep) {
+              if (fill && r + row < T) cp_async16_or_zero(in, st + S::kXOff + r * S::kStride, in ? b : xc);
+              b += step;
+            }
+          }
         }
+        cp_async_arrive(ring.full());
+        ring.next();
       }
     }
+    cp_async_wait_all();
+    return;
+  }
+
+  // ------------------------------------------------------------------------- product warps
+  const int wc = warp - 4, tid = threadIdx.x - 128;
+  auto sync = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+  if constexpr (FUSED) {
+    // 8, 4, 2 or 1 warps a row
+    const int per = T == 1 ? 8 : T == 2 ? 4 : T <= 4 ? 2 : 1, j = wc / per, sub = (wc % per) * 32 + lane;
+    const TX* x = static_cast<const TX*>(p.x) + static_cast<int64_t>(min(j, T - 1)) * p.ldx;
+    uint32_t amax = 0;
+#pragma unroll 4
+    for (int k = sub; k < K; k += 32 * per) amax = max(amax, magnitude_bits(to_f32(x[k])));
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    if (lane == 0) part[wc] = amax;
+    sync();
+    for (int w = j * per; w < (j + 1) * per; ++w) amax = max(amax, part[w]);
+    const float s = int8_scale(amax), inv = 1.0f / s;
+    if (j < T) {
+      if (sub == 0) xs[j] = s;
+      uint8_t* q = smem + S::kRedBytes + j * S::xstride(K);
+#pragma unroll 1
+      for (int k = sub * 8; k < ((K + 63) & ~63); k += 256 * per) {
+        uint2 w = make_uint2(0u, 0u);
+        if (k < K) {
+          float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int s = __reduce_add_sync(0xffffffffu, acc[j]);
-      if (lane == j && t0 + j < T)
-        out[static_cast<int64_t>(t0 + j) * ldo + n] = from_f32<TOut>(static_cast<float>(s) * (sx[t0 + j] * sw[n]));
+          for (int i = 0; i < 8; ++i) v[i] = to_f32(x[k + i]);
+          w = int8_codes8(v, s, inv);
+        }
+        *reinterpret_cast<uint2*>(q + k) = w;
+      }
+    }
+  } else {
+    for (int j = tid; j < T; j += 256) xs[j] = p.x_scale[j];
+  }
+  sync();
+  const int grp = wc / S::kSplit, ks = wc % S::kSplit;
+  const int g = lane >> 2, t = lane & 3;
+  int* red = reinterpret_cast<int*>(smem);
+  for (; !c.done(); c.next()) {
+    int acc[2][NT][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0;
+#pragma unroll 1
+    for (int k0 = 0; k0 < K; k0 += S::KC) {
+      few_mbar_wait(ring.full(), ring.phase, abort, p.status, 0xC10u + ring.stage);
+      __syncwarp();
+      const uint32_t st = ring.addr();
+      const uint32_t w = st + (32 * grp + g) * S::kStride + t * 16u;
+      const uint32_t x = (FUSED ? xq + k0 : st + S::kXOff) + t * 16u;
+      const uint32_t xstride = FUSED ? S::xstride(K) : S::kStride;
+      const int units = (min(S::KC, K - k0) + 63) / 64;
+#pragma unroll 1
+      for (int u = ks; u < units; u += S::kSplit) {
+        uint4 a[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = lds128(w + 8u * i * S::kStride + 64u * u);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          // (rows past the last token are not staged, their columns not used)
+          const uint4 b = lds128(x + min(8 * n + g, T - 1) * xstride + 64u * u);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            mma_s8_16832(acc[m][n], a[2 * m].x, a[2 * m + 1].x, a[2 * m].y, a[2 * m + 1].y, b.x, b.y);
+            mma_s8_16832(acc[m][n], a[2 * m].z, a[2 * m + 1].z, a[2 * m].w, a[2 * m + 1].w, b.z, b.w);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ring.empty());
+      ring.next();
+    }
+    // 16 tokens at a time: red[warp][token][row], then a warp per token and row group
+#pragma unroll
+    for (int n0 = 0; n0 < NT; n0 += 2) {
+      if (8 * n0 >= T) break;
+      int* mine = red + wc * 16 * 33;
+#pragma unroll
+      for (int n = n0; n < n0 + 2 && n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mine[(8 * (n - n0) + 2 * t + (i & 1)) * 33 + 16 * m + 8 * (i >> 1) + g] = acc[m][n][i];
+      sync();
+      const int tokens = min(16, T - 8 * n0);
+      for (int i = wc; i < tokens * S::kGroups; i += 8) {
+        const int j = i / S::kGroups, gr = i % S::kGroups;
+        int v = 0;
+#pragma unroll
+        for (int q = 0; q < S::kSplit; ++q) v += red[((gr * S::kSplit + q) * 16 + j) * 33 + lane];
+        const int n = 32 * gr + lane;
+        if (n < c.len)
+          static_cast<TOut*>(p.out)[static_cast<int64_t>(8 * n0 + j) * p.ldo + c.f + n] =
+              from_f32<TOut>(static_cast<float>(v) * (xs[8 * n0 + j] * p.w_scale[c.f + n]));
+      }
+      sync();
     }
   }
 }

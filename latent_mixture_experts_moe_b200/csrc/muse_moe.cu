@@ -1358,16 +1358,47 @@ muse_status int8_gemm(const void* xc, const float* xs, int64_t T, int64_t K, con
   return MUSE_OK;
 }
 
+template <int NT, bool FUSED, typename TX, typename TOut>
+muse_status launch_int8_stream(Int8StreamArgs& a, cudaStream_t st) {
+  using S = Int8Stream<NT, FUSED>;
+  auto kern = k_int8_stream<NT, FUSED, TX, TOut>;
+  constexpr size_t kSmem = 227 * 1024 - 2 * 1024;  // less the static shared memory
+  const size_t fixed = S::kRedBytes + (FUSED ? align_up(a.T * S::xstride(a.K), 128) : 0);
+  const uint32_t stage = S::stage_bytes(a.T);
+  a.stages = static_cast<int>(std::min<size_t>(kFewMaxStages, (kSmem - fixed) / stage));
+  const size_t smem = fixed + a.stages * static_cast<size_t>(stage);
+  MUSE_CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+  kern<<<std::min(a.N, sm_count()), S::kThreads, smem, st>>>(a);
+  MUSE_CK(cudaGetLastError());
+  return MUSE_OK;
+}
+
+Int8StreamArgs int8_stream_args(const void* x, int64_t ldx, const float* xs, int64_t T, int64_t K,
+                                const muse_int8_weight& w, int64_t N, void* out, int64_t ldo, uint32_t* status) {
+  return {x, ldx, xs, static_cast<const int8_t*>(w.codes), w.scales, out, ldo, static_cast<int>(T),
+          static_cast<int>(K), static_cast<int>(N), 0, status};
+}
+
 template <typename TOut>
 muse_status int8_product(const void* xc, const float* xs, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
                          void* out, int64_t ldo, uint32_t* status, cudaStream_t st) {
   if (T > 64) return int8_gemm<TOut>(xc, xs, T, K, w, N, out, ldo, status, st);
-  const dim3 grid(static_cast<unsigned>(cdiv(N, 8)), static_cast<unsigned>(std::min<int64_t>(cdiv(T, 8), 65535)));
-  k_int8_matmul<TOut><<<grid, 256, 0, st>>>(static_cast<const int8_t*>(xc), xs, static_cast<int>(T),
-                                            static_cast<int>(K), static_cast<const int8_t*>(w.codes), w.scales,
-                                            static_cast<int>(N), static_cast<TOut*>(out), ldo);
-  MUSE_CK(cudaGetLastError());
-  return MUSE_OK;
+  Int8StreamArgs a = int8_stream_args(xc, K, xs, T, K, w, N, out, ldo, status);
+  if (T <= 8) return launch_int8_stream<1, false, float, TOut>(a, st);
+  if (T <= 16) return launch_int8_stream<2, false, float, TOut>(a, st);
+  if (T <= 32) return launch_int8_stream<4, false, float, TOut>(a, st);
+  return launch_int8_stream<8, false, float, TOut>(a, st);
+}
+
+// float rows, few enough that the product quantises them itself
+bool int8_fused(int64_t T, int64_t K) { return T <= 8 && T * Int8Stream<1, true>::xstride(static_cast<int>(K)) <= kInt8FusedBytes; }
+
+template <typename TX>
+muse_status int8_linear_fused(const void* x, int64_t ldx, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
+                              void* out, int32_t out_dtype, int64_t ldo, uint32_t* status, cudaStream_t st) {
+  Int8StreamArgs a = int8_stream_args(x, ldx, nullptr, T, K, w, N, out, ldo, status);
+  return out_dtype == MUSE_BF16 ? launch_int8_stream<1, true, TX, __nv_bfloat16>(a, st)
+                                : launch_int8_stream<1, true, TX, float>(a, st);
 }
 
 // the sizes, weights and output of an int8 product
@@ -1709,6 +1740,12 @@ muse_status muse_int8_linear(const void* x, int32_t x_dtype, int64_t T, int64_t 
   size_t need = 0;
   MUSE_TRY(muse_int8_linear_workspace_size(T, K, &need));
   if (!aligned_to(workspace, kAlign) || workspace_bytes < need) return MUSE_ERR_WORKSPACE;
+  if (int8_fused(T, K)) {
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return x_dtype == MUSE_BF16
+               ? int8_linear_fused<__nv_bfloat16>(x, ldx, T, K, *w, N, out, out_dtype, ldo, status, st)
+               : int8_linear_fused<float>(x, ldx, T, K, *w, N, out, out_dtype, ldo, status, st);
+  }
   float* scales = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align_up(static_cast<size_t>(T * K), kAlign));
   MUSE_TRY(quantize_int8(x, x_dtype, T, K, ldx, workspace, scales, static_cast<cudaStream_t>(stream)));
   return muse_int8_matmul(workspace, scales, T, K, w, N, out, out_dtype, ldo, status, stream);
