@@ -37,7 +37,6 @@
 
 #include <cstdint>
 #include <cuda_bf16.h>
-#include <type_traits>
 
 #include "ptx.cuh"
 
@@ -75,7 +74,7 @@ struct GemmArgs {
   const float* w_scale;      // int8 operands: scale of each output feature
   int plain_store;           // CTA-pair kernel, int8 operands: outputs that TMA cannot store (row
                              // distance or start not on 16 bytes) leave by plain stores
-  int bn;                    // dense tiling: tokens per tile, a multiple of 32 (0: the kernel's largest)
+  int bn;                    // CTA-pair kernel, dense tiling: tokens per tile, a multiple of 32 (0: 256)
 };
 
 // Split-K decode of launch tile t (dense tiling): range s = t / base of base tile t % base,
@@ -103,10 +102,6 @@ struct ElemTraits<__nv_bfloat16> {
   static constexpr uint32_t kFmt = 1;  // bf16
 };
 template <>
-struct ElemTraits<int8_t> {
-  static constexpr bool kTF32 = false;
-};
-template <>
 struct ElemTraits<float> {
   static constexpr bool kTF32 = true;
   static constexpr uint32_t kFmt = 2;  // tf32
@@ -120,18 +115,6 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <>
 __device__ __forceinline__ float from_f32<float>(float v) { return v; }
-
-// An accumulator as the product's value: int8 operands' 32-bit sums times the scales of the row
-// and the feature (the sum rounded once to float32), the others' FP32 sums as they are.
-template <typename TIn>
-__device__ __forceinline__ float acc_value(uint32_t acc, float scale) {
-  if constexpr (sizeof(TIn) == 1) return static_cast<float>(static_cast<int32_t>(acc)) * scale;
-  return __uint_as_float(acc);
-}
-// The token scales of a chunk of 32 accumulator columns, one per lane (int8 operands).
-__device__ __forceinline__ float chunk_scale(const GemmArgs& p, int row0, int c, int n, int lane) {
-  return c * 32 + lane < n ? p.x_scale[row0 + c * 32 + lane] : 0.0f;
-}
 
 // MT = 128-row weight tiles per CTA: 2 puts two accumulators behind one token tile
 // (gate and up for EPI_SWIGLU; two adjacent 128-feature blocks otherwise), which halves
@@ -183,9 +166,6 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& p, int t, int BN, int&
     n = min(BN, p.T - row0);
   }
 }
-
-// tokens per tile of a dense launch
-__device__ __forceinline__ int tile_tokens(const GemmArgs& p, int BN) { return p.bn > 0 ? p.bn : BN; }
 
 // Sum over the 32 lanes of each of 32 registers: afterwards lane l holds the total of
 // register l (butterfly exchange of halves, 31 shuffles for 32 sums).
@@ -270,7 +250,7 @@ __global__ void __launch_bounds__(192, 1) k_umma_gemm(const __grid_constant__ Tm
       for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
         int g, m0, row0, n, tb = t, ks, kb0, kb1;
         split_range(p, num_tiles, tb, ks, kb0, kb1);
-        gemm_tile(p, tb, tile_tokens(p, BN), g, m0, row0, n);
+        gemm_tile(p, tb, BN, g, m0, row0, n);
         const int nb16 = (n + 15) >> 4;
         const uint32_t bytes = S::kABytes * (kDual ? 2u : 1u) + static_cast<uint32_t>(nb16) * 2048u;
         const int a_row = g * p.rows_per_group + m0;
@@ -322,11 +302,9 @@ __global__ void __launch_bounds__(192, 1) k_umma_gemm(const __grid_constant__ Tm
       for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
         int g, m0, row0, n, tb = t, ks, kb0, kb1;
         split_range(p, num_tiles, tb, ks, kb0, kb1);
-        gemm_tile(p, tb, tile_tokens(p, BN), g, m0, row0, n);
+        gemm_tile(p, tb, BN, g, m0, row0, n);
         const uint32_t N = static_cast<uint32_t>((n + 15) & ~15);
-        uint32_t idesc;
-        if constexpr (sizeof(TIn) == 1) idesc = idesc_i8(128u, N);
-        else idesc = idesc_f32acc(ElemTraits<TIn>::kFmt, 128u, N);
+        const uint32_t idesc = idesc_f32acc(ElemTraits<TIn>::kFmt, 128u, N);
         if (!mbar_wait(acce_bar(acc), acc_phase ^ 1u, abort_flag, p.status, 0x200u + acc)) {
           ok = false;
           break;
@@ -345,13 +323,8 @@ __global__ void __launch_bounds__(192, 1) k_umma_gemm(const __grid_constant__ Tm
           for (int kk = 0; kk < 4; ++kk) {
             const uint32_t accum = (kb > kb0 || kk > 0) ? 1u : 0u;
             const uint64_t db = sdesc_k_sw128(sB + 32u * kk);
-            if constexpr (sizeof(TIn) == 1) {
-              umma_i8(d, sdesc_k_sw128(sA + 32u * kk), db, idesc, accum);
-              if (kDual) umma_i8(d + BN, sdesc_k_sw128(sA + S::kABytes + 32u * kk), db, idesc, accum);
-            } else {
-              umma<kTF32>(d, sdesc_k_sw128(sA + 32u * kk), db, idesc, accum);
-              if (kDual) umma<kTF32>(d + BN, sdesc_k_sw128(sA + S::kABytes + 32u * kk), db, idesc, accum);
-            }
+            umma<kTF32>(d, sdesc_k_sw128(sA + 32u * kk), db, idesc, accum);
+            if (kDual) umma<kTF32>(d + BN, sdesc_k_sw128(sA + S::kABytes + 32u * kk), db, idesc, accum);
           }
           issued_any = true;
           tc_commit(empty_bar(stage));
@@ -384,7 +357,7 @@ __global__ void __launch_bounds__(192, 1) k_umma_gemm(const __grid_constant__ Tm
     for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
       int g, m0, row0, n, tb = t, ks, kb0, kb1;
       split_range(p, num_tiles, tb, ks, kb0, kb1);
-      gemm_tile(p, tb, tile_tokens(p, BN), g, m0, row0, n);
+      gemm_tile(p, tb, BN, g, m0, row0, n);
       // every lane waits; the vote keeps the warp converged for the .sync.aligned loads
       const bool ready = mbar_wait(accf_bar(acc), acc_phase, abort_flag, p.status, 0x400u + acc);
       if (!__all_sync(0xffffffffu, ready)) break;
@@ -415,21 +388,12 @@ __global__ void __launch_bounds__(192, 1) k_umma_gemm(const __grid_constant__ Tm
           const int f = m0 + half * 128 + q * 32 + lane;
           const bool f_ok = f < p.m_valid;
           float gain1 = 1.0f;
-          using TGain = typename std::conditional<sizeof(TIn) == 1, TOut, TIn>::type;
           if (EPI == EPI_STORE_SS && p.ss_gain != nullptr && f_ok)
-            gain1 = 1.0f + to_f32(reinterpret_cast<const TGain*>(p.ss_gain)[g * p.ss_gain_group_stride + f]);
-          float wscale = 1.0f;
-          if (sizeof(TIn) == 1) wscale = f_ok ? p.w_scale[f] : 0.0f;
+            gain1 = 1.0f + to_f32(reinterpret_cast<const TIn*>(p.ss_gain)[g * p.ss_gain_group_stride + f]);
           for (int c = 0; c < nchunks; ++c) {
             uint32_t v[32];
             tmem_ld32(taddr + static_cast<uint32_t>(half * BN) + 32u * c, v);
             tmem_ld_wait();
-            if constexpr (sizeof(TIn) == 1) {
-              const float xs = chunk_scale(p, row0, c, n, lane);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                v[i] = __float_as_uint(acc_value<TIn>(v[i], __shfl_sync(0xffffffffu, xs, i) * wscale));
-            }
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const int tok = c * 32 + i;

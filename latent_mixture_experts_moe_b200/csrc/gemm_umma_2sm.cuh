@@ -34,6 +34,21 @@
 
 namespace muse {
 
+// An accumulator as the product's value: int8 operands' 32-bit sums times the scales of the row
+// and the feature (the sum rounded once to float32), the others' FP32 sums as they are.
+template <typename TIn>
+__device__ __forceinline__ float acc_value(uint32_t acc, float scale) {
+  if constexpr (sizeof(TIn) == 1) return static_cast<float>(static_cast<int32_t>(acc)) * scale;
+  return __uint_as_float(acc);
+}
+// The token scales of a chunk of 32 accumulator columns, one per lane (int8 operands).
+__device__ __forceinline__ float chunk_scale(const GemmArgs& p, int row0, int c, int n, int lane) {
+  return c * 32 + lane < n ? p.x_scale[row0 + c * 32 + lane] : 0.0f;
+}
+
+// tokens per tile of a dense launch
+__device__ __forceinline__ int tile_tokens(const GemmArgs& p, int BN) { return p.bn > 0 ? p.bn : BN; }
+
 template <int EPI, int MT>
 struct Gemm2Shape {
   static constexpr bool kDual = (MT == 2);
@@ -129,6 +144,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // partner barriers are initialised before anyone signals them
+  if constexpr (kInt8) wait_for_predecessor();  // the rows' quantiser
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   const int num_tiles = (p.tiles != nullptr) ? *p.num_tiles_dev : p.num_tiles;

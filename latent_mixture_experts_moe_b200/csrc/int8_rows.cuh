@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(256, 5) k_quant_rows_int8(const T* __restrict_
   const int sub = threadIdx.x % TPR;
   const int r = blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
   if (r >= rows) return;  // (all threads of the row)
+  let_dependents_start();
   const T* x = src + static_cast<int64_t>(r) * ld;
   int8_t* out = codes + static_cast<int64_t>(r) * K;
   Int8Load<T, ALIGNED> hold[kVecs];
@@ -145,23 +146,23 @@ __global__ void __launch_bounds__(256, 5) k_quant_rows_int8(const T* __restrict_
   if (sub == 0) scales[r] = s;
 }
 
-// The product of at most 64 rows: weight rows streamed once, as in few_tokens.cuh. The channels
-// are divided evenly over the CTAs (one per SM). Four producer warps fill a ring of stages, R
+// The product of at most 16 rows: weight rows streamed once, as in few_tokens.cuh. The channels
+// are divided evenly over the CTAs (one per SM). Four producer warps fill a ring of stages, 32
 // weight rows and the activation rows x KC bytes of K, by 16-byte asynchronous copies. Eight
-// product warps (R / 32 groups of 32 rows, each splitting K) run m16n8k32 integer MMAs: weight
-// rows as A, eight tokens as B's columns; lane (g, t) reads 16 consecutive bytes of rows g and
-// g + 8 and of token g, and K's order is that of these bytes in both operands. Past K the
-// activations are zeros. The warps' sums are added through shared memory, 16 tokens at a time.
-// FUSED (at most 8 float rows): every CTA quantises the rows itself while its ring fills, one
-// launch less and no round trip through memory.
-// Bound by reading the weights; with 64 rows by the activations every SM fetches too (R = 64
-// halves those), and 4.3 GOP at the warp-level integer MMA's 1.1 POPS (measured) are 3.8 us.
+// product warps split K and run m16n8k32 integer MMAs: weight rows as A, eight tokens as B's
+// columns; lane (g, t) reads 16 consecutive bytes of rows g and g + 8 and of token g, and K's order
+// is that of these bytes in both operands. Past K the activations are zeros. The warps' sums are
+// added through shared memory.
+// FUSED (float rows, as many as eight warps can hold in registers): every CTA quantises the rows
+// itself while its ring fills, one launch less and no round trip through memory.
+// Bound by reading the weights: one row through 4096 x 8192 weights in 6.0 us (5.6 TB/s). From 17
+// rows on the split-K kernel is faster (64 rows: 10 us, against 27 here: every SM fetches all rows).
+constexpr int kInt8StreamRows = 16;
 template <int NT, bool FUSED>
 struct Int8Stream {
-  static constexpr int R = NT >= 4 ? 64 : 32;                      // weight rows of a stage
-  static constexpr int KC = NT >= 4 ? 256 : NT == 2 ? 512 : 1024;  // bytes of K of a stage
-  static constexpr int kGroups = R / 32, kSplit = 8 / kGroups;     // row groups; product warps per group
-  static constexpr uint32_t kStride = KC + 64;                     // see FewGeo on bank conflicts
+  static constexpr int R = 32;                        // weight rows of a stage
+  static constexpr int KC = NT == 2 ? 512 : 1024;     // bytes of K of a stage
+  static constexpr uint32_t kStride = KC + 64;        // see FewGeo on bank conflicts
   static constexpr uint32_t kXOff = R * kStride;
   static constexpr uint32_t stage_bytes(int T) { return (kXOff + (FUSED ? 0 : T) * kStride + 127) / 128 * 128; }
   static constexpr uint32_t kRedBytes = 8u * 16u * 33u * 4u;
@@ -169,7 +170,9 @@ struct Int8Stream {
   // fused: distance of the quantised rows
   __host__ __device__ static constexpr uint32_t xstride(int K) { return static_cast<uint32_t>((K + 127) / 128 * 128 + 64); }
 };
-constexpr int kInt8FusedBytes = 72 * 1024;  // quantised rows a fused call may hold
+// fused: warps that share a row, and the longest row they hold (8 x 8 values a thread)
+__host__ __device__ constexpr int int8_row_warps(int T) { return T == 1 ? 8 : T == 2 ? 4 : T <= 4 ? 2 : 1; }
+__host__ __device__ constexpr int int8_fused_depth(int T) { return 64 * 32 * int8_row_warps(T); }
 
 struct Int8StreamArgs {
   const void* x;            // codes [T, K], or (fused) float rows ldx apart
@@ -180,6 +183,7 @@ struct Int8StreamArgs {
   void* out;
   int64_t ldo;
   int T, K, N, stages;
+  bool after_quantiser;     // (for the host: how it is launched)
   uint32_t* status;
 };
 
@@ -241,6 +245,7 @@ __global__ void __launch_bounds__(Int8Stream<NT, FUSED>::kThreads, 1) k_int8_str
             a += step;
           }
           if constexpr (!FUSED) {
+            if (k0 == 0) wait_for_predecessor();
             // (a unit of K is 64 bytes: zeros up to its end)
             const int8_t* b = xc + k0;
             const bool fill = k0 + o < ((K + 63) & ~63);
@@ -263,12 +268,24 @@ __global__ void __launch_bounds__(Int8Stream<NT, FUSED>::kThreads, 1) k_int8_str
   const int wc = warp - 4, tid = threadIdx.x - 128;
   auto sync = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
   if constexpr (FUSED) {
-    // 8, 4, 2 or 1 warps a row
-    const int per = T == 1 ? 8 : T == 2 ? 4 : T <= 4 ? 2 : 1, j = wc / per, sub = (wc % per) * 32 + lane;
+    const int per = int8_row_warps(T), j = wc / per, sub = (wc % per) * 32 + lane;
     const TX* x = static_cast<const TX*>(p.x) + static_cast<int64_t>(min(j, T - 1)) * p.ldx;
+    Int8Load<TX, true> hold[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = (i * 32 * per + sub) * 8;
+      if (k < K) hold[i].load(x + k);
+    }
     uint32_t amax = 0;
-#pragma unroll 4
-    for (int k = sub; k < K; k += 32 * per) amax = max(amax, magnitude_bits(to_f32(x[k])));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((i * 32 * per + sub) * 8 < K) {
+        float v[8];
+        hold[i].get(v);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) amax = max(amax, magnitude_bits(v[q]));
+      }
+    }
     amax = __reduce_max_sync(0xffffffffu, amax);
     if (lane == 0) part[wc] = amax;
     sync();
@@ -277,23 +294,22 @@ __global__ void __launch_bounds__(Int8Stream<NT, FUSED>::kThreads, 1) k_int8_str
     if (j < T) {
       if (sub == 0) xs[j] = s;
       uint8_t* q = smem + S::kRedBytes + j * S::xstride(K);
-#pragma unroll 1
-      for (int k = sub * 8; k < ((K + 63) & ~63); k += 256 * per) {
-        uint2 w = make_uint2(0u, 0u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = (i * 32 * per + sub) * 8;
         if (k < K) {
           float v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = to_f32(x[k + i]);
-          w = int8_codes8(v, s, inv);
+          hold[i].get(v);
+          *reinterpret_cast<uint2*>(q + k) = int8_codes8(v, s, inv);
         }
-        *reinterpret_cast<uint2*>(q + k) = w;
       }
+      if (sub < 8 && K + 8 * sub < ((K + 63) & ~63)) *reinterpret_cast<uint2*>(q + K + 8 * sub) = make_uint2(0u, 0u);
     }
   } else {
+    wait_for_predecessor();
     for (int j = tid; j < T; j += 256) xs[j] = p.x_scale[j];
   }
   sync();
-  const int grp = wc / S::kSplit, ks = wc % S::kSplit;
   const int g = lane >> 2, t = lane & 3;
   int* red = reinterpret_cast<int*>(smem);
   for (; !c.done(); c.next()) {
@@ -309,12 +325,12 @@ __global__ void __launch_bounds__(Int8Stream<NT, FUSED>::kThreads, 1) k_int8_str
       few_mbar_wait(ring.full(), ring.phase, abort, p.status, 0xC10u + ring.stage);
       __syncwarp();
       const uint32_t st = ring.addr();
-      const uint32_t w = st + (32 * grp + g) * S::kStride + t * 16u;
+      const uint32_t w = st + g * S::kStride + t * 16u;
       const uint32_t x = (FUSED ? xq + k0 : st + S::kXOff) + t * 16u;
       const uint32_t xstride = FUSED ? S::xstride(K) : S::kStride;
       const int units = (min(S::KC, K - k0) + 63) / 64;
-#pragma unroll 1
-      for (int u = ks; u < units; u += S::kSplit) {
+#pragma unroll 2
+      for (int u = wc; u < units; u += 8) {
         uint4 a[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] = lds128(w + 8u * i * S::kStride + 64u * u);
@@ -333,32 +349,25 @@ __global__ void __launch_bounds__(Int8Stream<NT, FUSED>::kThreads, 1) k_int8_str
       if (lane == 0) mbar_arrive(ring.empty());
       ring.next();
     }
-    // 16 tokens at a time: red[warp][token][row], then a warp per token and row group
+    // red[warp][token][row]
+    int* mine = red + wc * 16 * 33;
 #pragma unroll
-    for (int n0 = 0; n0 < NT; n0 += 2) {
-      if (8 * n0 >= T) break;
-      int* mine = red + wc * 16 * 33;
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = n0; n < n0 + 2 && n < NT; ++n)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int i = 0; i < 4; ++i)
+          mine[(8 * n + 2 * t + (i & 1)) * 33 + 16 * m + 8 * (i >> 1) + g] = acc[m][n][i];
+    sync();
+    for (int j = wc; j < T; j += 8) {
+      int v = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mine[(8 * (n - n0) + 2 * t + (i & 1)) * 33 + 16 * m + 8 * (i >> 1) + g] = acc[m][n][i];
-      sync();
-      const int tokens = min(16, T - 8 * n0);
-      for (int i = wc; i < tokens * S::kGroups; i += 8) {
-        const int j = i / S::kGroups, gr = i % S::kGroups;
-        int v = 0;
-#pragma unroll
-        for (int q = 0; q < S::kSplit; ++q) v += red[((gr * S::kSplit + q) * 16 + j) * 33 + lane];
-        const int n = 32 * gr + lane;
-        if (n < c.len)
-          static_cast<TOut*>(p.out)[static_cast<int64_t>(8 * n0 + j) * p.ldo + c.f + n] =
-              from_f32<TOut>(static_cast<float>(v) * (xs[8 * n0 + j] * p.w_scale[c.f + n]));
-      }
-      sync();
+      for (int q = 0; q < 8; ++q) v += red[(q * 16 + j) * 33 + lane];
+      if (lane < c.len)
+        static_cast<TOut*>(p.out)[static_cast<int64_t>(j) * p.ldo + c.f + lane] =
+            from_f32<TOut>(static_cast<float>(v) * (xs[j] * p.w_scale[c.f + lane]));
     }
+    sync();
   }
 }
 

@@ -26,6 +26,7 @@
 #include "gemm_umma_w4a4.cuh"
 #include "gemv_fp4.cuh"
 #include "int8_rows.cuh"
+#include "int8_splitk.cuh"
 #include "nvfp4_act.cuh"
 #include "route_kernels.cuh"
 
@@ -361,9 +362,9 @@ bool make_w4a4_maps(W4A4Maps* m, const muse_nvfp4_weight* w, const muse_nvfp4_we
          make_u8_map(&m->sfb, scales, R, K / 16, 16, bn, false);
 }
 
-template <typename TOut, int EPI, int MT, typename TIn = __nv_bfloat16>
+template <typename TOut, int EPI, int MT>
 cudaError_t launch_gemm_2sm(const TmaMaps& maps, const GemmArgs& args, int pairs, cudaStream_t st) {
-  auto kern = k_umma_gemm_2sm<TOut, EPI, MT, TIn>;
+  auto kern = k_umma_gemm_2sm<TOut, EPI, MT>;
   const size_t smem = Gemm2Shape<EPI, MT>::kSmemBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -1279,36 +1280,94 @@ muse_status quantize_int8(const void* src, int32_t dtype, int64_t rows, int64_t 
                             : quantize_int8_t(static_cast<const float*>(src), rows, K, ld, c, scales, st);
 }
 
-// How an int8 product of many rows is tiled: on CTA pairs (256 mt features x tokens) or single CTAs
-// (128 x tokens). A tile's clocks per 128-byte k-block are those of its MMAs (2 per token and 256
-// features) or of fetching its operands (128 mt weight rows and all, on a pair half, of its token
-// rows, at the ~48 bytes a clock an SM gets from L2), whichever is more; with two accumulators (mt =
-// 2) the epilogue, ~20 clocks a token, is not hidden behind the next tile. The plan with the least
-// sum over its waves wins.
+// How an int8 product of many rows is tiled: on CTA pairs (256 mt features x tokens), or with K
+// split over clusters of `splits` CTAs (128 features x tokens, int8_splitk.cuh). A tile's clocks
+// per 128-byte k-block are those of its MMAs (2 per token and 256 features) or of fetching its
+// operands (128 mt weight rows and all, on a pair half, of its token rows, at the ~48 bytes a
+// clock an SM gets from L2 by TMA), whichever is more; with two accumulators (mt = 2) the
+// epilogue, ~20 clocks a token, is not hidden behind the next tile; the split tiles' exchange
+// costs ~4000 clocks. The plan with the least sum over its waves wins.
 struct Int8Plan {
-  bool pair;
-  int mt, tokens;
+  int mt, tokens, splits;  // mt = 0: split K
 };
 Int8Plan int8_plan(int64_t T, int64_t N, int64_t K) {
   const int nsm = sm_count();
-  Int8Plan best{true, 1, 256};
+  const int64_t kb = cdiv(K, 128);
+  Int8Plan best{1, 256, 1};
   int64_t best_cost = INT64_MAX;
-  for (int tokens = 256; tokens >= 32; tokens -= 32)
-    for (int mt = 2; mt >= 0; --mt) {  // 0: a single CTA
-      const int64_t tiles = cdiv(T, tokens) * cdiv(N, mt ? 256 * mt : 128), slots = mt ? nsm / 2 : nsm;
-      const int64_t mma = 2 * tokens * std::max(mt, 1), load = (128 * std::max(mt, 1) + (mt ? tokens / 2 : tokens)) * 8 / 3;
-      const int64_t cost = cdiv(tiles, slots) * (cdiv(K, 128) * std::max(mma, load) + (mt == 2 ? 20 * tokens : 0) + 1500);
-      if (cost < best_cost) {
-        best_cost = cost;
-        best = {mt != 0, std::max(mt, 1), tokens};
-      }
+  auto consider = [&](int64_t cost, const Int8Plan& plan) {
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = plan;
     }
+  };
+  for (int tokens = 256; tokens >= 32; tokens -= 32) {
+    for (int mt = 2; mt >= 1; --mt) {
+      const int64_t tiles = cdiv(T, tokens) * cdiv(N, 256 * mt);
+      const int64_t mma = 2 * tokens * mt, load = (128 * mt + tokens / 2) * 8 / 3;
+      consider(cdiv(tiles, nsm / 2) * (kb * std::max(mma, load) + (mt == 2 ? 20 * tokens : 0) + 1500), {mt, tokens, 1});
+    }
+    for (int splits = 1; splits <= 8 && 2 * splits <= kb; splits *= 2) {
+      const int64_t tiles = cdiv(T, tokens) * cdiv(N, 128) * splits;
+      const int64_t clocks = std::max<int64_t>(2 * tokens, (128 + tokens) * 8 / 3);
+      consider(cdiv(tiles, nsm / splits * splits) * (cdiv(kb, splits) * clocks + 4000), {0, tokens, splits});
+    }
+  }
   return best;
+}
+
+// A launch that may start while the kernel before it on the stream, the rows' quantiser, still runs
+// (it waits for its results itself); cluster: CTAs per cluster along x, 0 for the kernel's own.
+struct Int8Launch {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attrs[2];
+  Int8Launch(dim3 grid, int threads, size_t smem, cudaStream_t st, bool after_quantiser, int cluster = 0) {
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 0;
+    if (cluster > 0) {
+      cudaLaunchAttribute& c = attrs[cfg.numAttrs++];
+      c.id = cudaLaunchAttributeClusterDimension;
+      c.val.clusterDim.x = static_cast<unsigned>(cluster);
+      c.val.clusterDim.y = c.val.clusterDim.z = 1;
+    }
+    if (after_quantiser) {
+      cudaLaunchAttribute& a = attrs[cfg.numAttrs++];
+      a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      a.val.programmaticStreamSerializationAllowed = 1;
+    }
+  }
+};
+
+template <int BN, typename TOut>
+muse_status launch_int8_splitk(const TmaMaps& maps, const Int8SplitArgs& a, int tiles, int splits, bool after_quantiser,
+                               cudaStream_t st) {
+  auto kern = k_int8_splitk<BN, TOut>;
+  const size_t smem = Int8SplitShape<BN>::kSmemBytes;
+  MUSE_CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+  Int8Launch l(dim3(static_cast<unsigned>(splits), static_cast<unsigned>(tiles), 1), 192, smem, st, after_quantiser,
+               splits);
+  MUSE_CK(cudaLaunchKernelEx(&l.cfg, kern, maps, a));
+  return MUSE_OK;
+}
+
+template <typename TOut, int EPI, int MT>
+cudaError_t launch_int8_pair(const TmaMaps& maps, const GemmArgs& args, int pairs, bool after_quantiser, cudaStream_t st) {
+  auto kern = k_umma_gemm_2sm<TOut, EPI, MT, int8_t>;
+  const size_t smem = Gemm2Shape<EPI, MT>::kSmemBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  Int8Launch l(dim3(2 * pairs), kPairThreads, smem, st, after_quantiser);
+  return cudaLaunchKernelEx(&l.cfg, kern, maps, args);
 }
 
 template <typename TOut, int EPI = EPI_STORE>
 muse_status int8_gemm(const void* xc, const float* xs, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
-                      void* out, int64_t ldo, uint32_t* status, cudaStream_t st, DenseSS sq = DenseSS{}) {
+                      void* out, int64_t ldo, uint32_t* status, bool after_quantiser, cudaStream_t st,
+                      DenseSS sq = DenseSS{}) {
   if (encode_fn() == nullptr) return MUSE_ERR_CUDA;
   const Int8Plan plan = int8_plan(T, N, K);
   TmaMaps maps;
@@ -1318,7 +1377,6 @@ muse_status int8_gemm(const void* xc, const float* xs, int64_t T, int64_t K, con
   for (int i = 0; i < 5; ++i)
     if (!make_u8_map(&maps.b[i], xc, T, K, 128, 16 << i, true)) return MUSE_ERR_CUDA;
   GemmArgs g = base_args(status);
-  const int nsm = sm_count();
   g.m_valid = static_cast<int>(N);
   g.T = static_cast<int>(T);
   g.k_blocks = static_cast<int>(cdiv(K, 128));
@@ -1331,30 +1389,32 @@ muse_status int8_gemm(const void* xc, const float* xs, int64_t T, int64_t K, con
   g.ss_gain = sq.gain;
   // token chunks as equal as possible
   g.bn = static_cast<int>(align_up(static_cast<size_t>(cdiv(T, cdiv(T, plan.tokens))), 32));
-  g.m_step = plan.pair ? 256 * plan.mt : 128;
+  if constexpr (EPI == EPI_STORE) {
+    if (plan.mt == 0) {
+      const int m_tiles = static_cast<int>(cdiv(N, 128));
+      const int bn = static_cast<int>(align_up(static_cast<size_t>(cdiv(T, cdiv(T, plan.tokens))), 16));
+      const int64_t tiles = m_tiles * cdiv(T, bn);
+      if (tiles <= 65535) {
+        const Int8SplitArgs a{xs, w.scales, out, ldo, static_cast<int>(T), static_cast<int>(N), g.k_blocks, m_tiles, bn, status};
+        if (bn <= 64) return launch_int8_splitk<64, TOut>(maps, a, static_cast<int>(tiles), plan.splits, after_quantiser, st);
+        if (bn <= 128) return launch_int8_splitk<128, TOut>(maps, a, static_cast<int>(tiles), plan.splits, after_quantiser, st);
+        return launch_int8_splitk<256, TOut>(maps, a, static_cast<int>(tiles), plan.splits, after_quantiser, st);
+      }
+    }
+  }
+  const int mt = std::max(plan.mt, 1);
+  g.m_step = 256 * mt;
   g.m_tiles = static_cast<int>(cdiv(N, g.m_step));
   g.num_tiles = static_cast<int>(g.m_tiles * cdiv(T, g.bn));
-  if (plan.pair) {
-    // (bf16 tiles leave by TMA where the output's rows start on 16 bytes)
-    if constexpr (sizeof(TOut) == 2) {
-      g.plain_store = !aligned16(out) || ldo % 8 != 0;
-      if (!g.plain_store && !make_out_map(&maps.out, out, T, N, ldo)) return MUSE_ERR_CUDA;
-    }
-    if (N >= T)
-      g.m_group = static_cast<int>(std::max<int64_t>(1, (int64_t(32) << 20) / (g.m_step * K)));
-    const int pairs = std::min(g.num_tiles, nsm / 2);
-    if (plan.mt == 2) MUSE_CK((launch_gemm_2sm<TOut, EPI, 2, int8_t>(maps, g, pairs, st)));
-    else MUSE_CK((launch_gemm_2sm<TOut, EPI, 1, int8_t>(maps, g, pairs, st)));
-    return MUSE_OK;
+  // (bf16 tiles leave by TMA where the output's rows start on 16 bytes)
+  if constexpr (sizeof(TOut) == 2) {
+    g.plain_store = !aligned16(out) || ldo % 8 != 0;
+    if (!g.plain_store && !make_out_map(&maps.out, out, T, N, ldo)) return MUSE_ERR_CUDA;
   }
-  const int grid = std::min(g.num_tiles, nsm);
-  if (g.bn <= 32) {
-    MUSE_CK((launch_gemm<int8_t, TOut, 32, EPI, 1>(maps, g, grid, st)));
-  } else if (g.bn <= 128) {
-    MUSE_CK((launch_gemm<int8_t, TOut, 128, EPI, 1>(maps, g, grid, st)));
-  } else {
-    MUSE_CK((launch_gemm<int8_t, TOut, 256, EPI, 1>(maps, g, grid, st)));
-  }
+  if (N >= T) g.m_group = static_cast<int>(std::max<int64_t>(1, (int64_t(32) << 20) / (g.m_step * K)));
+  const int pairs = std::min(g.num_tiles, sm_count() / 2);
+  if (mt == 2) MUSE_CK((launch_int8_pair<TOut, EPI, 2>(maps, g, pairs, after_quantiser, st)));
+  else MUSE_CK((launch_int8_pair<TOut, EPI, 1>(maps, g, pairs, after_quantiser, st)));
   return MUSE_OK;
 }
 
@@ -1368,35 +1428,45 @@ muse_status launch_int8_stream(Int8StreamArgs& a, cudaStream_t st) {
   a.stages = static_cast<int>(std::min<size_t>(kFewMaxStages, (kSmem - fixed) / stage));
   const size_t smem = fixed + a.stages * static_cast<size_t>(stage);
   MUSE_CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-  kern<<<std::min(a.N, sm_count()), S::kThreads, smem, st>>>(a);
-  MUSE_CK(cudaGetLastError());
+  Int8Launch l(dim3(std::min(a.N, sm_count())), S::kThreads, smem, st, a.after_quantiser);
+  MUSE_CK(cudaLaunchKernelEx(&l.cfg, kern, static_cast<const Int8StreamArgs&>(a)));
   return MUSE_OK;
 }
 
+// x: codes with their scales xs, or float rows ldx apart (xs null) that the product quantises
 Int8StreamArgs int8_stream_args(const void* x, int64_t ldx, const float* xs, int64_t T, int64_t K,
-                                const muse_int8_weight& w, int64_t N, void* out, int64_t ldo, uint32_t* status) {
+                                const muse_int8_weight& w, int64_t N, void* out, int64_t ldo, uint32_t* status,
+                                bool after_quantiser) {
   return {x, ldx, xs, static_cast<const int8_t*>(w.codes), w.scales, out, ldo, static_cast<int>(T),
-          static_cast<int>(K), static_cast<int>(N), 0, status};
+          static_cast<int>(K), static_cast<int>(N), 0, after_quantiser, status};
 }
 
+// after_quantiser: the codes' quantiser was launched just before on the stream
 template <typename TOut>
 muse_status int8_product(const void* xc, const float* xs, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
-                         void* out, int64_t ldo, uint32_t* status, cudaStream_t st) {
-  if (T > 64) return int8_gemm<TOut>(xc, xs, T, K, w, N, out, ldo, status, st);
-  Int8StreamArgs a = int8_stream_args(xc, K, xs, T, K, w, N, out, ldo, status);
-  if (T <= 8) return launch_int8_stream<1, false, float, TOut>(a, st);
-  if (T <= 16) return launch_int8_stream<2, false, float, TOut>(a, st);
-  if (T <= 32) return launch_int8_stream<4, false, float, TOut>(a, st);
-  return launch_int8_stream<8, false, float, TOut>(a, st);
+                         void* out, int64_t ldo, uint32_t* status, bool after_quantiser, cudaStream_t st) {
+  if (T > kInt8StreamRows) return int8_gemm<TOut>(xc, xs, T, K, w, N, out, ldo, status, after_quantiser, st);
+  Int8StreamArgs a = int8_stream_args(xc, K, xs, T, K, w, N, out, ldo, status, after_quantiser);
+  return T <= 8 ? launch_int8_stream<1, false, float, TOut>(a, st) : launch_int8_stream<2, false, float, TOut>(a, st);
+}
+muse_status int8_product(const void* xc, const float* xs, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
+                         void* out, int32_t out_dtype, int64_t ldo, uint32_t* status, bool after_quantiser,
+                         cudaStream_t st) {
+  return out_dtype == MUSE_BF16
+             ? int8_product<__nv_bfloat16>(xc, xs, T, K, w, N, out, ldo, status, after_quantiser, st)
+             : int8_product<float>(xc, xs, T, K, w, N, out, ldo, status, after_quantiser, st);
 }
 
-// float rows, few enough that the product quantises them itself
-bool int8_fused(int64_t T, int64_t K) { return T <= 8 && T * Int8Stream<1, true>::xstride(static_cast<int>(K)) <= kInt8FusedBytes; }
+// float rows that the product can quantise itself: few and short enough for its registers
+bool int8_fused(const void* x, int32_t dtype, int64_t T, int64_t K, int64_t ldx) {
+  return T <= 8 && K <= int8_fused_depth(static_cast<int>(T)) && aligned16(x) &&
+         (T == 1 || ldx * static_cast<int64_t>(dtype_size(dtype)) % 16 == 0);
+}
 
 template <typename TX>
 muse_status int8_linear_fused(const void* x, int64_t ldx, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
                               void* out, int32_t out_dtype, int64_t ldo, uint32_t* status, cudaStream_t st) {
-  Int8StreamArgs a = int8_stream_args(x, ldx, nullptr, T, K, w, N, out, ldo, status);
+  Int8StreamArgs a = int8_stream_args(x, ldx, nullptr, T, K, w, N, out, ldo, status, false);
   return out_dtype == MUSE_BF16 ? launch_int8_stream<1, true, TX, __nv_bfloat16>(a, st)
                                 : launch_int8_stream<1, true, TX, float>(a, st);
 }
@@ -1718,8 +1788,7 @@ muse_status muse_int8_matmul(const void* x_codes, const float* x_scales, int64_t
   if (T == 0) return MUSE_OK;
   if (!aligned_to(x_codes, 16) || !aligned_to(x_scales, 4)) return MUSE_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return out_dtype == MUSE_BF16 ? int8_product<__nv_bfloat16>(x_codes, x_scales, T, K, *w, N, out, ldo, status, st)
-                                : int8_product<float>(x_codes, x_scales, T, K, *w, N, out, ldo, status, st);
+  return int8_product(x_codes, x_scales, T, K, *w, N, out, out_dtype, ldo, status, false, st);
 }
 
 muse_status muse_int8_linear_workspace_size(int64_t T, int64_t K, size_t* bytes) {
@@ -1740,15 +1809,14 @@ muse_status muse_int8_linear(const void* x, int32_t x_dtype, int64_t T, int64_t 
   size_t need = 0;
   MUSE_TRY(muse_int8_linear_workspace_size(T, K, &need));
   if (!aligned_to(workspace, kAlign) || workspace_bytes < need) return MUSE_ERR_WORKSPACE;
-  if (int8_fused(T, K)) {
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (int8_fused(x, x_dtype, T, K, ldx))
     return x_dtype == MUSE_BF16
                ? int8_linear_fused<__nv_bfloat16>(x, ldx, T, K, *w, N, out, out_dtype, ldo, status, st)
                : int8_linear_fused<float>(x, ldx, T, K, *w, N, out, out_dtype, ldo, status, st);
-  }
   float* scales = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align_up(static_cast<size_t>(T * K), kAlign));
-  MUSE_TRY(quantize_int8(x, x_dtype, T, K, ldx, workspace, scales, static_cast<cudaStream_t>(stream)));
-  return muse_int8_matmul(workspace, scales, T, K, w, N, out, out_dtype, ldo, status, stream);
+  MUSE_TRY(quantize_int8(x, x_dtype, T, K, ldx, workspace, scales, st));
+  return int8_product(workspace, scales, T, K, *w, N, out, out_dtype, ldo, status, true, st);
 }
 
 muse_status muse_latent_moe_few_tokens_workspace_size(const muse_moe_config* cfg, size_t* bytes) {

@@ -349,6 +349,13 @@ __device__ __forceinline__ void epilogue_group_bar_sync(int grp) {
   asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory");
 }
 
+// ------------------------------------------------------------------------ dependent launches
+// Programmatic dependent launch: a kernel lets the one that follows it on the stream start, and
+// that one waits for the first one's results where it needs them (not at all, if it was
+// launched without such an edge).
+__device__ __forceinline__ void let_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------------------ CTA pairs
 // (cluster of 2 CTAs on one TPC driving cta_group::2 MMAs; still no multicast loads)
 __device__ __forceinline__ uint32_t cluster_ctarank() {
