@@ -458,7 +458,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
             const float tot = transpose_reduce32(yv, lane);
             const int tok = c * 32 + lane;
-            if (tok < n) p.ss[(static_cast<int64_t>(row0) + tok) * p.ss_ld + ((col_cta + h * 256) >> 5) + q] = tot;
+            // (a width that is no multiple of 256 leaves the last tile's second CTA without features)
+            if (tok < n && col_cta + h * 256 < p.m_valid)
+              p.ss[(static_cast<int64_t>(row0) + tok) * p.ss_ld + ((col_cta + h * 256) >> 5) + q] = tot;
           }
         };
         uint32_t va[32], vb[32];
