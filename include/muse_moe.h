@@ -103,6 +103,18 @@ typedef enum muse_norm_mode {
   MUSE_NORM_INPUT_SCALED = 1  /* u / sqrt(mean(u^2)+eps), u = y * (1+gamma)           */
 } muse_norm_mode;
 
+/* Format of the two dense projections W_pool and W_unpool. */
+typedef enum muse_proj_weights {
+  MUSE_PROJ_DENSE = 0,        /* tensors of cfg->dtype                                   */
+  MUSE_PROJ_INT8 = 1          /* each points to a muse_int8_weight (below): W_pool codes
+                                 [L, D], scales [L]; W_unpool codes [D, L], scales [D].
+                                 Every token's row of the projection's input (x, or xn;
+                                 the combined latent c as stored in cfg->dtype) is
+                                 quantised to int8 with a scale of its own, the product
+                                 is exact in 32-bit integers; the router reads the rows
+                                 as they are                                             */
+} muse_proj_weights;
+
 /* Block configuration. Zero-initialise, then set the sizes; muse_moe_config_init
  * fills the defaults (softmax router, centred per-expert norm, eps 1e-6). */
 typedef struct muse_moe_config {
@@ -151,6 +163,7 @@ typedef struct muse_moe_config {
   float residual_gate_temperature; /* pages: 0.3                                      */
   float residual_gate_eps;    /* floor of alpha^2; pages: 1e-3                         */
   int32_t act_format;         /* muse_act_format of the expert GEMMs' activations      */
+  int32_t proj_weights;       /* muse_proj_weights                                    */
 } muse_moe_config;
 
 /* Byte offsets of the intermediates inside the workspace after a forward call, for
@@ -196,7 +209,8 @@ MUSE_API muse_status muse_latent_moe_workspace_layout(const muse_moe_config* cfg
 
 /* Forward pass of the block on device buffers (layouts above); enqueued on `stream`
  * (with cfg->expert_weights == MUSE_EXPERTS_NVFP4, W_gate / W_up / W_down are host
- * pointers to muse_nvfp4_weight descriptions of device tensors)
+ * pointers to muse_nvfp4_weight descriptions of device tensors; with cfg->proj_weights ==
+ * MUSE_PROJ_INT8, W_pool / W_unpool are host pointers to muse_int8_weight)
  * (a cudaStream_t, NULL = legacy default stream). Pointers must be device memory,
  * 16-byte aligned; `out` must not alias an input. Returns without synchronising. */
 MUSE_API muse_status muse_latent_moe_forward(const muse_moe_config* cfg, const void* x,
@@ -209,7 +223,9 @@ MUSE_API muse_status muse_latent_moe_forward(const muse_moe_config* cfg, const v
  * type, rank, extents and strides (in elements, outermost first). The library reads
  * row-major contiguous tensors only: strides must be the contiguous ones
  * (stride[ndim-1] = 1, stride[i] = stride[i+1] * shape[i+1]). */
-typedef enum muse_elem_type { MUSE_ELEM_F32 = 0, MUSE_ELEM_BF16 = 1, MUSE_ELEM_U8 = 2 } muse_elem_type;
+typedef enum muse_elem_type {
+  MUSE_ELEM_F32 = 0, MUSE_ELEM_BF16 = 1, MUSE_ELEM_U8 = 2, MUSE_ELEM_I8 = 3
+} muse_elem_type;
 typedef struct muse_tensor {
   const void* data;           /* device memory, 16-byte aligned                        */
   int32_t elem;               /* muse_elem_type (F32 / BF16 match muse_dtype)          */
@@ -227,7 +243,9 @@ typedef struct muse_tensor {
  * all of element type cfg->dtype, contiguous, 16-byte aligned; out may not overlap any
  * input. With cfg->expert_weights == MUSE_EXPERTS_NVFP4, W_gate / W_up / W_down each point
  * to THREE consecutive descriptors -- codes u8 [E, out, in/2], block scales u8 [E, out,
- * in/16], matrix scales f32 [E] -- and the forward receives them as muse_nvfp4_weight.
+ * in/16], matrix scales f32 [E] -- and the forward receives them as muse_nvfp4_weight. With
+ * cfg->proj_weights == MUSE_PROJ_INT8, W_pool and W_unpool each point to TWO: codes i8 [out,
+ * in], scales f32 [out].
  * Any mismatch returns MUSE_ERR_INVALID_ARG with nothing launched; otherwise the result
  * is that of muse_latent_moe_forward on the same pointers. */
 MUSE_API muse_status muse_latent_moe_forward_checked(const muse_moe_config* cfg, const muse_tensor* x,
@@ -372,7 +390,7 @@ MUSE_API muse_status muse_int8_linear(const void* x, int32_t x_dtype, int64_t T,
  * expert outputs and the sublayer's f stay FP32, float32 workloads multiply in FP32 (not
  * TF32), and with NVFP4 experts the latent is rounded to f16 once. It requires 16-bit or
  * float32 activations (MUSE_ACT_NVFP4 is UNSUPPORTED); NVFP4 experts require L and I
- * multiples of 256. stage_events is ignored. cfg->workspace: device, 256-byte aligned,
+ * multiples of 256; int8 projections are UNSUPPORTED. stage_events is ignored. cfg->workspace: device, 256-byte aligned,
  * muse_latent_moe_few_tokens_workspace_size bytes, a layout of its own; calls whose work
  * overlaps on the GPU need workspaces of their own. The kernel is launched cooperatively
  * (its CTAs, one per SM, wait for one another): MUSE_ERR_CUDA where the device cannot hold
@@ -480,9 +498,10 @@ MUSE_API const char* muse_last_cuda_error(void);
 
 /* Number of stages one forward call runs for cfg -- the positions of stage_events -- and
  * the name of stage i (a static string; NULL past the last). In order: [ffn_pre_norm],
- * router, topk, expert_hist, tiles, assign_rows, pooler, [pre_expert_norm], gather (with
- * W4A4 activations: quant_z, gather_codes), gate_up_swiglu, [quant_h (W4A4)], down_sumsq,
- * norm_combine, unpooler, [ffn_post_norm_gate]. Each stage is
+ * router, topk, expert_hist, tiles, assign_rows, [quant_x (int8 projections)], pooler,
+ * [pre_expert_norm], gather (with W4A4 activations: quant_z, gather_codes), gate_up_swiglu,
+ * [quant_h (W4A4)], down_sumsq, norm_combine, [quant_c (int8 projections)], unpooler,
+ * [ffn_post_norm_gate]. Each stage is
  * one kernel, except that a dense GEMM (router, pooler, unpooler) whose tiles would fill
  * less than half the SMs splits K and adds a partial-sum kernel inside its stage
  * (decode-sized token counts). stage_events must hold launch_count + 1 events. -1 / NULL

@@ -20,6 +20,7 @@ ROUTER_SOFTMAX, ROUTER_SIGMOID = 0, 1
 EXPERTS_DENSE, EXPERTS_NVFP4 = 0, 1
 ACT_BF16, ACT_NVFP4 = 0, 1
 NORM_CENTRED, NORM_INPUT_SCALED = 0, 1
+PROJ_DENSE, PROJ_INT8 = 0, 1
 
 STATUS = {0: "MUSE_OK", 1: "MUSE_ERR_INVALID_ARG", 2: "MUSE_ERR_UNSUPPORTED", 3: "MUSE_ERR_WORKSPACE",
           4: "MUSE_ERR_CUDA", 5: "MUSE_ERR_TIMEOUT", 6: "MUSE_ERR_DEVICE"}
@@ -67,7 +68,8 @@ class Config(ctypes.Structure):
                 ("ffn_pre_gain", ctypes.c_void_p), ("ffn_pre_eps", ctypes.c_float),
                 ("ffn_post_gain", ctypes.c_void_p), ("ffn_post_eps", ctypes.c_float),
                 ("residual_gate", ctypes.c_void_p), ("residual_gate_temperature", ctypes.c_float),
-                ("residual_gate_eps", ctypes.c_float), ("act_format", ctypes.c_int32)]
+                ("residual_gate_eps", ctypes.c_float), ("act_format", ctypes.c_int32),
+                ("proj_weights", ctypes.c_int32)]
 
 
 class Tensor(ctypes.Structure):
@@ -76,14 +78,14 @@ class Tensor(ctypes.Structure):
                 ("shape", ctypes.c_int64 * 3), ("stride", ctypes.c_int64 * 3)]
 
 
-ELEM_F32, ELEM_BF16, ELEM_U8 = 0, 1, 2
+ELEM_F32, ELEM_BF16, ELEM_U8, ELEM_I8 = 0, 1, 2, 3
 
 
 def tensor_desc(t) -> Tensor:
     """The muse_tensor of a torch tensor (its own shape and strides: a non-contiguous view
     is described as it is, and the library rejects it)."""
     import torch
-    elem = {torch.float32: ELEM_F32, torch.bfloat16: ELEM_BF16, torch.uint8: ELEM_U8}.get(t.dtype, -1)
+    elem = {torch.float32: ELEM_F32, torch.bfloat16: ELEM_BF16, torch.uint8: ELEM_U8, torch.int8: ELEM_I8}.get(t.dtype, -1)
     return Tensor(t.data_ptr(), elem, t.dim(), tuple(t.shape[:3]), tuple(t.stride()[:3]))
 
 
@@ -251,14 +253,16 @@ def forward(cfg: Config, x, W_router, W_pool, W_gate, W_up, W_down, gamma, W_unp
 def forward_checked(cfg: Config, x, W_router, W_pool, W_gate, W_up, W_down, gamma, W_unpool, out,
                     stream=None) -> None:
     """Enqueue one forward through the shape-checked entry point: every argument is a torch
-    tensor (NVFP4 experts: a (codes, block scales, matrix scales) triple each) described by
+    tensor (NVFP4 experts: a (codes, block scales, matrix scales) triple each; int8
+    projections: a (codes, scales) pair each) described by
     its dtype, shape and strides; the library rejects a mismatch before launching anything."""
     _call_checked(lib().muse_latent_moe_forward_checked, "muse_latent_moe_forward_checked", cfg, x, W_router, W_pool,
                   W_gate, W_up, W_down, gamma, W_unpool, out, stream)
 
 
 def _weight_descs(W_router, W_pool, W_gate, W_up, W_down, gamma, W_unpool):
-    """The muse_tensor arrays of a layer's weights, in argument order (NVFP4 experts: three each)."""
+    """The muse_tensor arrays of a layer's weights, in argument order (NVFP4 experts: three each,
+    int8 projections: two each)."""
     def descs(t):
         parts = t if isinstance(t, (tuple, list)) else (t,)
         return (Tensor * len(parts))(*[tensor_desc(p) for p in parts])
@@ -529,6 +533,16 @@ def expert_operands(weights: Dict, nvfp4: bool):
                  for n in ("W_gate", "W_up", "W_down"))
 
 
+def projection_operand(weights: Dict, name: str):
+    """(W_pool or W_unpool as the C ABI takes it, as the shape-checked entry points take it): the
+    dense tensor, or for int8 weights <name>_codes [out, in] and <name>_scales [out] (of
+    quantize_int8_rows) an Int8Weight and the two tensors."""
+    if name + "_codes" not in weights:
+        return weights[name], weights[name]
+    codes, scales = weights[name + "_codes"], weights[name + "_scales"]
+    return Int8Weight(_ptr(codes), _ptr(scales)), (codes, scales)
+
+
 def block_config(T: int, dims: Dict, dtype: str, modes: Dict, weights: Dict, nvfp4: bool, workspace=None) -> Config:
     """Config of the block for T tokens: sizes, modes, the optional pointers found in
     weights (router_bias, pre_norm_gain, ffn_pre_gain, ffn_post_gain, residual_gate) and
@@ -537,6 +551,10 @@ def block_config(T: int, dims: Dict, dtype: str, modes: Dict, weights: Dict, nvf
     c = make_config(T, d["D"], d["L"], d["I"], d["E"], d["k"], dtype, d["eps"], **modes)
     if nvfp4:
         c.expert_weights = EXPERTS_NVFP4
+    if ("W_pool_codes" in weights) != ("W_unpool_codes" in weights):
+        raise ValueError("W_pool and W_unpool must both be int8 or both dense")
+    if "W_pool_codes" in weights:
+        c.proj_weights = PROJ_INT8
     if weights.get("router_bias") is not None:
         c.router_bias = _ptr(weights["router_bias"])
     for name in ("pre_norm_gain", "ffn_pre_gain", "ffn_post_gain", "residual_gate"):
@@ -553,7 +571,8 @@ class LatentMoE:
     the shape-checked entry point (muse_latent_moe_forward_checked).
 
     weights: dict with W_router, W_pool, W_gate, W_up, W_down, gamma, W_unpool (torch
-    CUDA tensors in the layouts of include/muse_moe.h); router_bias, pre_norm_gain and the
+    CUDA tensors in the layouts of include/muse_moe.h; int8 projections as W_pool_codes,
+    W_pool_scales, W_unpool_codes and W_unpool_scales instead, of quantize_int8_rows); router_bias, pre_norm_gain and the
     feed-forward sublayer's ffn_pre_gain, ffn_post_gain and residual_gate (float32) are
     optional. modes: make_config keywords (router_mode, norm_mode, gamma_shared, ...).
     """
@@ -567,6 +586,9 @@ class LatentMoE:
         self.experts = tuple((weights[n + "_codes"], weights[n + "_scales"], weights[n + "_mscale"]) if self.nvfp4
                              else weights[n] for n in ("W_gate", "W_up", "W_down"))
         self.w["W_gate"], self.w["W_up"], self.w["W_down"] = expert_operands(weights, self.nvfp4)
+        # the projections as the C ABI and as the shape-checked entry points take them
+        self.w["W_pool"], self.pool = projection_operand(weights, "W_pool")
+        self.w["W_unpool"], self.unpool = projection_operand(weights, "W_unpool")
         self.dtype = {torch.float32: "f32", torch.bfloat16: "bf16"}[weights["W_router"].dtype]
         self.dims = dict(D=int(D), L=L, I=I, E=int(E), k=k, eps=eps)
         self.modes = modes
@@ -585,8 +607,8 @@ class LatentMoE:
         # its configuration and the weights' descriptors, once: a call of a few microseconds would
         # otherwise spend more time on marshalling than on the GPU
         self._few_config = self.config(min(T_max, FEW_TOKENS), self.few_workspace)
-        self._few_weights = _weight_descs(weights["W_router"], weights["W_pool"], *self.experts, weights["gamma"],
-                                          weights["W_unpool"])
+        self._few_weights = _weight_descs(weights["W_router"], self.pool, *self.experts, weights["gamma"],
+                                          self.unpool)
 
     def config(self, T: int, workspace=None) -> Config:
         return block_config(T, self.dims, self.dtype, self.modes, self.w, self.nvfp4, workspace)
@@ -604,7 +626,7 @@ class LatentMoE:
         if out is None:
             out = torch.empty((T, self.dims["D"]), dtype=x.dtype, device=x.device)
         w = self.w
-        forward_checked(cfg, x, w["W_router"], w["W_pool"], *self.experts, w["gamma"], w["W_unpool"], out, stream)
+        forward_checked(cfg, x, w["W_router"], self.pool, *self.experts, w["gamma"], self.unpool, out, stream)
         return out
 
     def few_tokens(self, x, out=None, stream=None, topk_idx=None, topk_w=None):

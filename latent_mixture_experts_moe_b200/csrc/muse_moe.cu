@@ -64,6 +64,7 @@ struct Layout {
   muse_moe_workspace_layout pub;
   size_t tiles_gu, tiles_dn, ntiles;  // int4 lists; int[8]: tile counts [0..1], tile counters [4..7]
   size_t zt_codes, zt_scales;         // W4A4: the latent quantised in token order [T, L/2], [T, L/16]
+  size_t proj_codes, proj_scales;     // int8 projections: a projection's input rows [T, max(D, L)], [T]
   size_t splitk, splitk_bytes;        // FP32 partial products of split-K dense GEMMs (0 bytes: none)
   int64_t max_tiles_gu, max_tiles_dn;
 };
@@ -124,6 +125,9 @@ Layout make_layout(const muse_moe_config& c, Role role = Role::kFull) {
   l.pub.zq_scales = take(q, rows * (c.L / 16));
   l.pub.hq_codes = take(q, rows * (c.I / 2));
   l.pub.hq_scales = take(q, rows * (c.I / 16));
+  const bool int8 = home && c.proj_weights == MUSE_PROJ_INT8;
+  l.proj_codes = take(int8, T * std::max(c.D, c.L));
+  l.proj_scales = take(int8, sizeof(float) * T);
   // split-K partials of the dense GEMMs (router, pooler, unpooler) when one of them has a K
   // of 64 k-blocks or more: up to 32 ranges of T x M floats, at most 8 MiB -- decode-sized
   // outputs; larger ones cost more in partial traffic than the extra CTAs win
@@ -160,6 +164,7 @@ muse_status validate_sizes(const muse_moe_config* c) {
   if (c->act_format == MUSE_ACT_NVFP4 &&
       (c->expert_weights != MUSE_EXPERTS_NVFP4 || c->L % 256 != 0 || c->I % 256 != 0))
     return MUSE_ERR_UNSUPPORTED;
+  if (c->proj_weights != MUSE_PROJ_DENSE && c->proj_weights != MUSE_PROJ_INT8) return MUSE_ERR_INVALID_ARG;
   return MUSE_OK;
 }
 
@@ -167,6 +172,14 @@ bool valid_nvfp4(const void* w) {
   const muse_nvfp4_weight* q = static_cast<const muse_nvfp4_weight*>(w);
   return q != nullptr && q->codes != nullptr && q->block_scales != nullptr && q->matrix_scale != nullptr &&
          aligned16(q->codes) && aligned16(q->block_scales) && (reinterpret_cast<uintptr_t>(q->matrix_scale) & 3u) == 0;
+}
+
+// a projection's weights: a dense tensor, or the description of int8 ones
+bool valid_projection(const muse_moe_config& c, const void* w) {
+  if (c.proj_weights != MUSE_PROJ_INT8) return w != nullptr && aligned16(w);
+  const muse_int8_weight* q = static_cast<const muse_int8_weight*>(w);
+  return q != nullptr && q->codes != nullptr && q->scales != nullptr && aligned16(q->codes) &&
+         (reinterpret_cast<uintptr_t>(q->scales) & 3u) == 0;
 }
 
 // ---------------------------------------------------------------------- tensor maps
@@ -525,6 +538,224 @@ thread_local cudaError_t g_last_cuda_error = cudaSuccess;
     if (s_ != MUSE_OK) return s_;       \
   } while (0)
 
+// ---------------------------------------------------------------------- int8 products
+bool aligned_to(const void* p, size_t a) { return p != nullptr && reinterpret_cast<uintptr_t>(p) % a == 0; }
+size_t dtype_size(int32_t dtype) { return dtype == MUSE_BF16 ? 2 : 4; }
+bool valid_dtype(int32_t dtype) { return dtype == MUSE_F32 || dtype == MUSE_BF16; }
+
+template <typename T>
+muse_status quantize_int8_t(const T* src, int64_t rows, int64_t K, int64_t ld, int8_t* codes, float* scales,
+                            cudaStream_t st) {
+  const bool aligned = aligned16(src) && (rows == 1 || ld * static_cast<int64_t>(sizeof(T)) % 16 == 0);
+  const int n = static_cast<int>(rows), k = static_cast<int>(K);
+  // as many threads as hold the row at 32 values each, at most a block
+  const int tpr = K <= 32 * 32 ? 32 : K <= 32 * 128 ? 128 : 256;
+  auto kern = tpr == 32    ? (aligned ? k_quant_rows_int8<T, 32, true> : k_quant_rows_int8<T, 32, false>)
+              : tpr == 128 ? (aligned ? k_quant_rows_int8<T, 128, true> : k_quant_rows_int8<T, 128, false>)
+                           : (aligned ? k_quant_rows_int8<T, 256, true> : k_quant_rows_int8<T, 256, false>);
+  kern<<<static_cast<unsigned>(cdiv(rows, 256 / tpr)), 256, 0, st>>>(src, ld, n, k, codes, scales);
+  MUSE_CK(cudaGetLastError());
+  return MUSE_OK;
+}
+
+muse_status quantize_int8(const void* src, int32_t dtype, int64_t rows, int64_t K, int64_t ld, void* codes,
+                          float* scales, cudaStream_t st) {
+  int8_t* c = static_cast<int8_t*>(codes);
+  return dtype == MUSE_BF16 ? quantize_int8_t(static_cast<const __nv_bfloat16*>(src), rows, K, ld, c, scales, st)
+                            : quantize_int8_t(static_cast<const float*>(src), rows, K, ld, c, scales, st);
+}
+
+// How an int8 product of many rows is tiled: on CTA pairs (256 mt features x tokens), or with K
+// split over clusters of `splits` CTAs (128 features x tokens, int8_splitk.cuh). A tile's clocks
+// per 128-byte k-block are those of its MMAs (2 per token and 256 features) or of fetching its
+// operands (128 mt weight rows and all, on a pair half, of its token rows, at the ~48 bytes a
+// clock an SM gets from L2 by TMA), whichever is more; with two accumulators (mt = 2) the
+// epilogue, ~20 clocks a token, is not hidden behind the next tile; the split tiles' exchange
+// costs ~4000 clocks. The plan with the least sum over its waves wins.
+struct Int8Plan {
+  int mt, tokens, splits;  // mt = 0: split K
+};
+Int8Plan int8_plan(int64_t T, int64_t N, int64_t K, bool may_split) {
+  const int nsm = sm_count();
+  const int64_t kb = cdiv(K, 128);
+  Int8Plan best{1, 256, 1};
+  int64_t best_cost = INT64_MAX;
+  auto consider = [&](int64_t cost, const Int8Plan& plan) {
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = plan;
+    }
+  };
+  for (int tokens = 256; tokens >= 32; tokens -= 32) {
+    for (int mt = 2; mt >= 1; --mt) {
+      const int64_t tiles = cdiv(T, tokens) * cdiv(N, 256 * mt);
+      const int64_t mma = 2 * tokens * mt, load = (128 * mt + tokens / 2) * 8 / 3;
+      consider(cdiv(tiles, nsm / 2) * (kb * std::max(mma, load) + (mt == 2 ? 20 * tokens : 0) + 1500), {mt, tokens, 1});
+    }
+    for (int splits = 1; may_split && splits <= 8 && 2 * splits <= kb; splits *= 2) {
+      const int64_t tiles = cdiv(T, tokens) * cdiv(N, 128) * splits;
+      const int64_t clocks = std::max<int64_t>(2 * tokens, (128 + tokens) * 8 / 3);
+      consider(cdiv(tiles, nsm / splits * splits) * (cdiv(kb, splits) * clocks + 4000), {0, tokens, splits});
+    }
+  }
+  return best;
+}
+
+// A launch that may start while the kernel before it on the stream, the rows' quantiser, still runs
+// (it waits for its results itself); cluster: CTAs per cluster along x, 0 for the kernel's own.
+struct Int8Launch {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attrs[2];
+  Int8Launch(dim3 grid, int threads, size_t smem, cudaStream_t st, bool after_quantiser, int cluster = 0) {
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 0;
+    if (cluster > 0) {
+      cudaLaunchAttribute& c = attrs[cfg.numAttrs++];
+      c.id = cudaLaunchAttributeClusterDimension;
+      c.val.clusterDim.x = static_cast<unsigned>(cluster);
+      c.val.clusterDim.y = c.val.clusterDim.z = 1;
+    }
+    if (after_quantiser) {
+      cudaLaunchAttribute& a = attrs[cfg.numAttrs++];
+      a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      a.val.programmaticStreamSerializationAllowed = 1;
+    }
+  }
+};
+
+template <int BN, typename TOut>
+muse_status launch_int8_splitk(const TmaMaps& maps, const Int8SplitArgs& a, int tiles, int splits, bool after_quantiser,
+                               cudaStream_t st) {
+  auto kern = k_int8_splitk<BN, TOut>;
+  const size_t smem = Int8SplitShape<BN>::kSmemBytes;
+  MUSE_CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+  Int8Launch l(dim3(static_cast<unsigned>(splits), static_cast<unsigned>(tiles), 1), 192, smem, st, after_quantiser,
+               splits);
+  MUSE_CK(cudaLaunchKernelEx(&l.cfg, kern, maps, a));
+  return MUSE_OK;
+}
+
+template <typename TOut, int EPI, int MT>
+cudaError_t launch_int8_pair(const TmaMaps& maps, const GemmArgs& args, int pairs, bool after_quantiser, cudaStream_t st) {
+  auto kern = k_umma_gemm_2sm<TOut, EPI, MT, int8_t>;
+  const size_t smem = Gemm2Shape<EPI, MT>::kSmemBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  Int8Launch l(dim3(2 * pairs), kPairThreads, smem, st, after_quantiser);
+  return cudaLaunchKernelEx(&l.cfg, kern, maps, args);
+}
+
+template <typename TOut, int EPI = EPI_STORE>
+muse_status int8_gemm(const void* xc, const float* xs, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
+                      void* out, int64_t ldo, uint32_t* status, bool after_quantiser, cudaStream_t st,
+                      DenseSS sq = DenseSS{}) {
+  if (encode_fn() == nullptr) return MUSE_ERR_CUDA;
+  const Int8Plan plan = int8_plan(T, N, K, EPI == EPI_STORE);
+  TmaMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  if (!make_u8_map(&maps.a, w.codes, N, K, 128, 128, true) || !make_u8_map(&maps.a2, w.codes, N, K, 128, 128, true))
+    return MUSE_ERR_CUDA;
+  for (int i = 0; i < 5; ++i)
+    if (!make_u8_map(&maps.b[i], xc, T, K, 128, 16 << i, true)) return MUSE_ERR_CUDA;
+  GemmArgs g = base_args(status);
+  g.m_valid = static_cast<int>(N);
+  g.T = static_cast<int>(T);
+  g.k_blocks = static_cast<int>(cdiv(K, 128));
+  g.out = out;
+  g.ld_out = ldo;
+  g.x_scale = xs;
+  g.w_scale = w.scales;
+  g.ss = sq.ss;
+  g.ss_ld = sq.ld;
+  g.ss_gain = sq.gain;
+  // token chunks as equal as possible
+  g.bn = static_cast<int>(align_up(static_cast<size_t>(cdiv(T, cdiv(T, plan.tokens))), 32));
+  if constexpr (EPI == EPI_STORE) {
+    if (plan.mt == 0) {
+      const int m_tiles = static_cast<int>(cdiv(N, 128));
+      const int bn = static_cast<int>(align_up(static_cast<size_t>(cdiv(T, cdiv(T, plan.tokens))), 16));
+      const int64_t tiles = m_tiles * cdiv(T, bn);
+      if (tiles <= 65535) {
+        const Int8SplitArgs a{xs, w.scales, out, ldo, static_cast<int>(T), static_cast<int>(N), g.k_blocks, m_tiles, bn, status};
+        if (bn <= 64) return launch_int8_splitk<64, TOut>(maps, a, static_cast<int>(tiles), plan.splits, after_quantiser, st);
+        if (bn <= 128) return launch_int8_splitk<128, TOut>(maps, a, static_cast<int>(tiles), plan.splits, after_quantiser, st);
+        return launch_int8_splitk<256, TOut>(maps, a, static_cast<int>(tiles), plan.splits, after_quantiser, st);
+      }
+    }
+  }
+  const int mt = std::max(plan.mt, 1);
+  g.m_step = 256 * mt;
+  g.m_tiles = static_cast<int>(cdiv(N, g.m_step));
+  g.num_tiles = static_cast<int>(g.m_tiles * cdiv(T, g.bn));
+  // (bf16 tiles leave by TMA where the output's rows start on 16 bytes)
+  if constexpr (sizeof(TOut) == 2) {
+    g.plain_store = !aligned16(out) || ldo % 8 != 0;
+    if (!g.plain_store && !make_out_map(&maps.out, out, T, N, ldo)) return MUSE_ERR_CUDA;
+  }
+  if (N >= T) g.m_group = static_cast<int>(std::max<int64_t>(1, (int64_t(32) << 20) / (g.m_step * K)));
+  const int pairs = std::min(g.num_tiles, sm_count() / 2);
+  if (mt == 2) MUSE_CK((launch_int8_pair<TOut, EPI, 2>(maps, g, pairs, after_quantiser, st)));
+  else MUSE_CK((launch_int8_pair<TOut, EPI, 1>(maps, g, pairs, after_quantiser, st)));
+  return MUSE_OK;
+}
+
+template <int NT, bool FUSED, typename TX, typename TOut>
+muse_status launch_int8_stream(Int8StreamArgs& a, cudaStream_t st) {
+  using S = Int8Stream<NT, FUSED>;
+  auto kern = k_int8_stream<NT, FUSED, TX, TOut>;
+  constexpr size_t kSmem = 227 * 1024 - 2 * 1024;  // less the static shared memory
+  const size_t fixed = S::kRedBytes + (FUSED ? align_up(a.T * S::xstride(a.K), 128) : 0);
+  const uint32_t stage = S::stage_bytes(a.T);
+  a.stages = static_cast<int>(std::min<size_t>(kFewMaxStages, (kSmem - fixed) / stage));
+  const size_t smem = fixed + a.stages * static_cast<size_t>(stage);
+  MUSE_CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+  Int8Launch l(dim3(std::min(a.N, sm_count())), S::kThreads, smem, st, a.after_quantiser);
+  MUSE_CK(cudaLaunchKernelEx(&l.cfg, kern, static_cast<const Int8StreamArgs&>(a)));
+  return MUSE_OK;
+}
+
+// x: codes with their scales xs, or float rows ldx apart (xs null) that the product quantises
+Int8StreamArgs int8_stream_args(const void* x, int64_t ldx, const float* xs, int64_t T, int64_t K,
+                                const muse_int8_weight& w, int64_t N, void* out, int64_t ldo, uint32_t* status,
+                                bool after_quantiser) {
+  return {x, ldx, xs, static_cast<const int8_t*>(w.codes), w.scales, out, ldo, static_cast<int>(T),
+          static_cast<int>(K), static_cast<int>(N), 0, after_quantiser, status};
+}
+
+// after_quantiser: the codes' quantiser was launched just before on the stream
+template <typename TOut>
+muse_status int8_product(const void* xc, const float* xs, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
+                         void* out, int64_t ldo, uint32_t* status, bool after_quantiser, cudaStream_t st) {
+  if (T > kInt8StreamRows) return int8_gemm<TOut>(xc, xs, T, K, w, N, out, ldo, status, after_quantiser, st);
+  Int8StreamArgs a = int8_stream_args(xc, K, xs, T, K, w, N, out, ldo, status, after_quantiser);
+  return T <= 8 ? launch_int8_stream<1, false, float, TOut>(a, st) : launch_int8_stream<2, false, float, TOut>(a, st);
+}
+muse_status int8_product(const void* xc, const float* xs, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
+                         void* out, int32_t out_dtype, int64_t ldo, uint32_t* status, bool after_quantiser,
+                         cudaStream_t st) {
+  return out_dtype == MUSE_BF16
+             ? int8_product<__nv_bfloat16>(xc, xs, T, K, w, N, out, ldo, status, after_quantiser, st)
+             : int8_product<float>(xc, xs, T, K, w, N, out, ldo, status, after_quantiser, st);
+}
+
+// float rows that the product can quantise itself: few and short enough for its registers
+bool int8_fused(const void* x, int32_t dtype, int64_t T, int64_t K, int64_t ldx) {
+  return T <= 8 && K <= int8_fused_depth(static_cast<int>(T)) && aligned16(x) &&
+         (T == 1 || ldx * static_cast<int64_t>(dtype_size(dtype)) % 16 == 0);
+}
+
+template <typename TX>
+muse_status int8_linear_fused(const void* x, int64_t ldx, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
+                              void* out, int32_t out_dtype, int64_t ldo, uint32_t* status, cudaStream_t st) {
+  Int8StreamArgs a = int8_stream_args(x, ldx, nullptr, T, K, w, N, out, ldo, status, false);
+  return out_dtype == MUSE_BF16 ? launch_int8_stream<1, true, TX, __nv_bfloat16>(a, st)
+                                : launch_int8_stream<1, true, TX, float>(a, st);
+}
+
 // One pass of kernels over a workspace: its buffers, the stream and the optional stage
 // events (recorded after each launch of the full forward; null on the expert-parallel
 // entry points).
@@ -652,14 +883,36 @@ muse_status permute(Pass<T>& p, const int* idx, int64_t n, int k) {
   return MUSE_OK;
 }
 
+// A projection with int8 weights: the rows [T, K] quantised, then the product [T, N].
+template <typename T>
+muse_status int8_projection(Pass<T>& p, const void* rows, int64_t K, const void* W, int64_t N, void* out,
+                            DenseSS sq = DenseSS{}) {
+  const muse_int8_weight& w = *static_cast<const muse_int8_weight*>(W);
+  uint8_t* codes = p.at(p.lay.proj_codes);
+  float* scales = p.template ptr<float>(p.lay.proj_scales);
+  MUSE_TRY(quantize_int8(rows, p.c.dtype, p.c.T, K, K, codes, scales, p.st));
+  MUSE_CK(p.mark());
+  const bool next = p.events == nullptr;  // (nothing between the two launches)
+  if (sq.ss != nullptr)
+    MUSE_TRY((int8_gemm<T, EPI_STORE_SS>(codes, scales, p.c.T, K, w, N, out, N, p.status, next, p.st, sq)));
+  else
+    MUSE_TRY((int8_product<T>(codes, scales, p.c.T, K, w, N, out, N, p.status, next, p.st)));
+  MUSE_CK(p.mark());
+  return MUSE_OK;
+}
+
 // (a4) pooler, then the pages' pre_expert_norm on z (optional)
 template <typename T>
 muse_status pool(Pass<T>& p, const void* xin, const void* W_pool) {
   const muse_moe_config& c = p.c;
   T* z = p.template ptr<T>(p.lay.pub.z);
-  MUSE_TRY((dense_gemm<T, T>(W_pool, c.L, xin, c.T, c.D, z, dense_bn(c), p.status, p.ntiles + 6, p.st, DenseSS{},
-                             p.splitk())));
-  MUSE_CK(p.mark());
+  if (c.proj_weights == MUSE_PROJ_INT8) {
+    MUSE_TRY((int8_projection<T>(p, xin, c.D, W_pool, c.L, z)));
+  } else {
+    MUSE_TRY((dense_gemm<T, T>(W_pool, c.L, xin, c.T, c.D, z, dense_bn(c), p.status, p.ntiles + 6, p.st, DenseSS{},
+                               p.splitk())));
+    MUSE_CK(p.mark());
+  }
   if (c.pre_norm_gain != nullptr) {
     k_rmsnorm_rows<T><<<static_cast<unsigned>(c.T), 256, 0, p.st>>>(
         z, z, reinterpret_cast<const T*>(c.pre_norm_gain), static_cast<int>(c.L), c.pre_norm_eps);
@@ -890,18 +1143,22 @@ muse_status combine(Pass<T>& p, const T* y, const float* ss, const void* x, cons
   // (a10) unpooler; with the sublayer post-norm its epilogue also writes the partial sums
   // of (f * (1 + w))^2
   const bool post = c.ffn_post_gain != nullptr;
+  DenseSS sq;
   if (post) {
-    DenseSS sq;
     sq.ss = p.template ptr<float>(p.lay.pub.ss_out);
     sq.ld = static_cast<int>(D / 32);
     sq.gain = c.ffn_post_gain;
+  }
+  if (c.proj_weights == MUSE_PROJ_INT8) {
+    MUSE_TRY((int8_projection<T>(p, cbuf, L, W_unpool, D, out, sq)));
+  } else if (post) {
     MUSE_TRY((dense_gemm<T, T, EPI_STORE_SS>(W_unpool, D, cbuf, Tn, L, out, dense_bn(c), p.status, p.ntiles + 7,
                                              p.st, sq)));
   } else {
     MUSE_TRY((dense_gemm<T, T>(W_unpool, D, cbuf, Tn, L, out, dense_bn(c), p.status, p.ntiles + 7, p.st, DenseSS{},
                                p.splitk())));
   }
-  MUSE_CK(p.mark());
+  if (c.proj_weights != MUSE_PROJ_INT8) MUSE_CK(p.mark());
   // feed-forward sublayer post-norm and residual gate (optional), in place on out
   if (post || c.residual_gate != nullptr) {
     const int vec = 16 / static_cast<int>(sizeof(T));
@@ -1099,29 +1356,55 @@ bool expert_tensor_is(const muse_moe_config& c, const muse_tensor* t, int64_t ro
   return true;
 }
 
-// The expert weights as the forward takes them, from their descriptors.
-struct ExpertOperands {
+// A projection [rows, cols]: one dense descriptor, or the two of int8 weights (codes, scales); fills
+// the weight the forward takes.
+bool projection_is(const muse_moe_config& c, const muse_tensor* t, int64_t rows, int64_t cols, muse_int8_weight* q,
+                   const void** w) {
+  if (c.proj_weights != MUSE_PROJ_INT8) {
+    if (!tensor_is(t, c.dtype, {rows, cols})) return false;
+    *w = t->data;
+    return true;
+  }
+  if (t == nullptr || !tensor_is(&t[0], MUSE_ELEM_I8, {rows, cols})) return false;
+  const muse_tensor* s = &t[1];  // float [rows], 4-byte aligned is enough for the kernels
+  if (s->data == nullptr || (reinterpret_cast<uintptr_t>(s->data) & 3u) || s->elem != MUSE_ELEM_F32 || s->ndim != 1 ||
+      s->shape[0] != rows || s->stride[0] != 1)
+    return false;
+  *q = muse_int8_weight{t[0].data, static_cast<const float*>(s->data)};
+  *w = q;
+  return true;
+}
+
+// The expert and projection weights as the forward takes them, from their descriptors.
+struct WeightOperands {
   muse_nvfp4_weight q[3];
-  const void *gate, *up, *down;
+  muse_int8_weight p[2];
+  const void *gate, *up, *down, *pool, *unpool;
 };
 
 // Every tensor of a forward against the configuration (see muse_latent_moe_forward_checked).
 muse_status check_tensors(const muse_moe_config& c, const muse_tensor* x, const muse_tensor* W_router,
                           const muse_tensor* W_pool, const muse_tensor* W_gate, const muse_tensor* W_up,
                           const muse_tensor* W_down, const muse_tensor* gamma, const muse_tensor* W_unpool,
-                          const muse_tensor* out, ExpertOperands* e) {
+                          const muse_tensor* out, WeightOperands* e) {
   const int32_t a = c.dtype;  // MUSE_F32 / MUSE_BF16 equal MUSE_ELEM_F32 / MUSE_ELEM_BF16
-  if (!tensor_is(x, a, {c.T, c.D}) || !tensor_is(W_router, a, {c.E, c.D}) || !tensor_is(W_pool, a, {c.L, c.D}) ||
-      !tensor_is(W_unpool, a, {c.D, c.L}) || !tensor_is(out, a, {c.T, c.D}))
+  if (!tensor_is(x, a, {c.T, c.D}) || !tensor_is(W_router, a, {c.E, c.D}) || !tensor_is(out, a, {c.T, c.D}) ||
+      !projection_is(c, W_pool, c.L, c.D, &e->p[0], &e->pool) ||
+      !projection_is(c, W_unpool, c.D, c.L, &e->p[1], &e->unpool))
     return MUSE_ERR_INVALID_ARG;
   if (!(c.gamma_shared ? tensor_is(gamma, a, {c.L}) : tensor_is(gamma, a, {c.E, c.L}))) return MUSE_ERR_INVALID_ARG;
   if (!expert_tensor_is(c, W_gate, c.I, c.L, &e->q[0], &e->gate) ||
       !expert_tensor_is(c, W_up, c.I, c.L, &e->q[1], &e->up) ||
       !expert_tensor_is(c, W_down, c.L, c.I, &e->q[2], &e->down))
     return MUSE_ERR_INVALID_ARG;
-  const muse_tensor* inputs[] = {x, W_router, W_pool, gamma, W_unpool};
+  const muse_tensor* inputs[] = {x, W_router, gamma};
   for (const muse_tensor* t : inputs)
     if (overlaps(out, t)) return MUSE_ERR_INVALID_ARG;
+  const int n_proj = c.proj_weights == MUSE_PROJ_INT8 ? 2 : 1;
+  const muse_tensor* projections[] = {W_pool, W_unpool};
+  for (const muse_tensor* t : projections)
+    for (int i = 0; i < n_proj; ++i)
+      if (overlaps(out, &t[i])) return MUSE_ERR_INVALID_ARG;
   const int n_exp = c.expert_weights == MUSE_EXPERTS_NVFP4 ? 3 : 1;
   const muse_tensor* experts[] = {W_gate, W_up, W_down};
   for (const muse_tensor* t : experts)
@@ -1140,7 +1423,8 @@ struct FewLayout {
 
 muse_status validate_few(const muse_moe_config* c) {
   MUSE_TRY(validate_sizes(c));
-  if (c->T > kFewTokens || c->act_format != MUSE_ACT_BF16) return MUSE_ERR_UNSUPPORTED;
+  if (c->T > kFewTokens || c->act_format != MUSE_ACT_BF16 || c->proj_weights != MUSE_PROJ_DENSE)
+    return MUSE_ERR_UNSUPPORTED;
   if (c->expert_weights == MUSE_EXPERTS_NVFP4 && (c->L % 256 != 0 || c->I % 256 != 0)) return MUSE_ERR_UNSUPPORTED;
   return MUSE_OK;
 }
@@ -1253,224 +1537,6 @@ muse_status few_tokens_impl(const muse_moe_config& c, const void* x, const void*
   return c.dtype == MUSE_BF16 ? launch_few<__nv_bfloat16, false>(a, st) : launch_few<float, false>(a, st);
 }
 
-// ---------------------------------------------------------------------- int8 products
-bool aligned_to(const void* p, size_t a) { return p != nullptr && reinterpret_cast<uintptr_t>(p) % a == 0; }
-size_t dtype_size(int32_t dtype) { return dtype == MUSE_BF16 ? 2 : 4; }
-bool valid_dtype(int32_t dtype) { return dtype == MUSE_F32 || dtype == MUSE_BF16; }
-
-template <typename T>
-muse_status quantize_int8_t(const T* src, int64_t rows, int64_t K, int64_t ld, int8_t* codes, float* scales,
-                            cudaStream_t st) {
-  const bool aligned = aligned16(src) && (rows == 1 || ld * static_cast<int64_t>(sizeof(T)) % 16 == 0);
-  const int n = static_cast<int>(rows), k = static_cast<int>(K);
-  // as many threads as hold the row at 32 values each, at most a block
-  const int tpr = K <= 32 * 32 ? 32 : K <= 32 * 128 ? 128 : 256;
-  auto kern = tpr == 32    ? (aligned ? k_quant_rows_int8<T, 32, true> : k_quant_rows_int8<T, 32, false>)
-              : tpr == 128 ? (aligned ? k_quant_rows_int8<T, 128, true> : k_quant_rows_int8<T, 128, false>)
-                           : (aligned ? k_quant_rows_int8<T, 256, true> : k_quant_rows_int8<T, 256, false>);
-  kern<<<static_cast<unsigned>(cdiv(rows, 256 / tpr)), 256, 0, st>>>(src, ld, n, k, codes, scales);
-  MUSE_CK(cudaGetLastError());
-  return MUSE_OK;
-}
-
-muse_status quantize_int8(const void* src, int32_t dtype, int64_t rows, int64_t K, int64_t ld, void* codes,
-                          float* scales, cudaStream_t st) {
-  int8_t* c = static_cast<int8_t*>(codes);
-  return dtype == MUSE_BF16 ? quantize_int8_t(static_cast<const __nv_bfloat16*>(src), rows, K, ld, c, scales, st)
-                            : quantize_int8_t(static_cast<const float*>(src), rows, K, ld, c, scales, st);
-}
-
-// How an int8 product of many rows is tiled: on CTA pairs (256 mt features x tokens), or with K
-// split over clusters of `splits` CTAs (128 features x tokens, int8_splitk.cuh). A tile's clocks
-// per 128-byte k-block are those of its MMAs (2 per token and 256 features) or of fetching its
-// operands (128 mt weight rows and all, on a pair half, of its token rows, at the ~48 bytes a
-// clock an SM gets from L2 by TMA), whichever is more; with two accumulators (mt = 2) the
-// epilogue, ~20 clocks a token, is not hidden behind the next tile; the split tiles' exchange
-// costs ~4000 clocks. The plan with the least sum over its waves wins.
-struct Int8Plan {
-  int mt, tokens, splits;  // mt = 0: split K
-};
-Int8Plan int8_plan(int64_t T, int64_t N, int64_t K) {
-  const int nsm = sm_count();
-  const int64_t kb = cdiv(K, 128);
-  Int8Plan best{1, 256, 1};
-  int64_t best_cost = INT64_MAX;
-  auto consider = [&](int64_t cost, const Int8Plan& plan) {
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = plan;
-    }
-  };
-  for (int tokens = 256; tokens >= 32; tokens -= 32) {
-    for (int mt = 2; mt >= 1; --mt) {
-      const int64_t tiles = cdiv(T, tokens) * cdiv(N, 256 * mt);
-      const int64_t mma = 2 * tokens * mt, load = (128 * mt + tokens / 2) * 8 / 3;
-      consider(cdiv(tiles, nsm / 2) * (kb * std::max(mma, load) + (mt == 2 ? 20 * tokens : 0) + 1500), {mt, tokens, 1});
-    }
-    for (int splits = 1; splits <= 8 && 2 * splits <= kb; splits *= 2) {
-      const int64_t tiles = cdiv(T, tokens) * cdiv(N, 128) * splits;
-      const int64_t clocks = std::max<int64_t>(2 * tokens, (128 + tokens) * 8 / 3);
-      consider(cdiv(tiles, nsm / splits * splits) * (cdiv(kb, splits) * clocks + 4000), {0, tokens, splits});
-    }
-  }
-  return best;
-}
-
-// A launch that may start while the kernel before it on the stream, the rows' quantiser, still runs
-// (it waits for its results itself); cluster: CTAs per cluster along x, 0 for the kernel's own.
-struct Int8Launch {
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attrs[2];
-  Int8Launch(dim3 grid, int threads, size_t smem, cudaStream_t st, bool after_quantiser, int cluster = 0) {
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = attrs;
-    cfg.numAttrs = 0;
-    if (cluster > 0) {
-      cudaLaunchAttribute& c = attrs[cfg.numAttrs++];
-      c.id = cudaLaunchAttributeClusterDimension;
-      c.val.clusterDim.x = static_cast<unsigned>(cluster);
-      c.val.clusterDim.y = c.val.clusterDim.z = 1;
-    }
-    if (after_quantiser) {
-      cudaLaunchAttribute& a = attrs[cfg.numAttrs++];
-      a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      a.val.programmaticStreamSerializationAllowed = 1;
-    }
-  }
-};
-
-template <int BN, typename TOut>
-muse_status launch_int8_splitk(const TmaMaps& maps, const Int8SplitArgs& a, int tiles, int splits, bool after_quantiser,
-                               cudaStream_t st) {
-  auto kern = k_int8_splitk<BN, TOut>;
-  const size_t smem = Int8SplitShape<BN>::kSmemBytes;
-  MUSE_CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-  Int8Launch l(dim3(static_cast<unsigned>(splits), static_cast<unsigned>(tiles), 1), 192, smem, st, after_quantiser,
-               splits);
-  MUSE_CK(cudaLaunchKernelEx(&l.cfg, kern, maps, a));
-  return MUSE_OK;
-}
-
-template <typename TOut, int EPI, int MT>
-cudaError_t launch_int8_pair(const TmaMaps& maps, const GemmArgs& args, int pairs, bool after_quantiser, cudaStream_t st) {
-  auto kern = k_umma_gemm_2sm<TOut, EPI, MT, int8_t>;
-  const size_t smem = Gemm2Shape<EPI, MT>::kSmemBytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  Int8Launch l(dim3(2 * pairs), kPairThreads, smem, st, after_quantiser);
-  return cudaLaunchKernelEx(&l.cfg, kern, maps, args);
-}
-
-template <typename TOut, int EPI = EPI_STORE>
-muse_status int8_gemm(const void* xc, const float* xs, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
-                      void* out, int64_t ldo, uint32_t* status, bool after_quantiser, cudaStream_t st,
-                      DenseSS sq = DenseSS{}) {
-  if (encode_fn() == nullptr) return MUSE_ERR_CUDA;
-  const Int8Plan plan = int8_plan(T, N, K);
-  TmaMaps maps;
-  std::memset(&maps, 0, sizeof(maps));
-  if (!make_u8_map(&maps.a, w.codes, N, K, 128, 128, true) || !make_u8_map(&maps.a2, w.codes, N, K, 128, 128, true))
-    return MUSE_ERR_CUDA;
-  for (int i = 0; i < 5; ++i)
-    if (!make_u8_map(&maps.b[i], xc, T, K, 128, 16 << i, true)) return MUSE_ERR_CUDA;
-  GemmArgs g = base_args(status);
-  g.m_valid = static_cast<int>(N);
-  g.T = static_cast<int>(T);
-  g.k_blocks = static_cast<int>(cdiv(K, 128));
-  g.out = out;
-  g.ld_out = ldo;
-  g.x_scale = xs;
-  g.w_scale = w.scales;
-  g.ss = sq.ss;
-  g.ss_ld = sq.ld;
-  g.ss_gain = sq.gain;
-  // token chunks as equal as possible
-  g.bn = static_cast<int>(align_up(static_cast<size_t>(cdiv(T, cdiv(T, plan.tokens))), 32));
-  if constexpr (EPI == EPI_STORE) {
-    if (plan.mt == 0) {
-      const int m_tiles = static_cast<int>(cdiv(N, 128));
-      const int bn = static_cast<int>(align_up(static_cast<size_t>(cdiv(T, cdiv(T, plan.tokens))), 16));
-      const int64_t tiles = m_tiles * cdiv(T, bn);
-      if (tiles <= 65535) {
-        const Int8SplitArgs a{xs, w.scales, out, ldo, static_cast<int>(T), static_cast<int>(N), g.k_blocks, m_tiles, bn, status};
-        if (bn <= 64) return launch_int8_splitk<64, TOut>(maps, a, static_cast<int>(tiles), plan.splits, after_quantiser, st);
-        if (bn <= 128) return launch_int8_splitk<128, TOut>(maps, a, static_cast<int>(tiles), plan.splits, after_quantiser, st);
-        return launch_int8_splitk<256, TOut>(maps, a, static_cast<int>(tiles), plan.splits, after_quantiser, st);
-      }
-    }
-  }
-  const int mt = std::max(plan.mt, 1);
-  g.m_step = 256 * mt;
-  g.m_tiles = static_cast<int>(cdiv(N, g.m_step));
-  g.num_tiles = static_cast<int>(g.m_tiles * cdiv(T, g.bn));
-  // (bf16 tiles leave by TMA where the output's rows start on 16 bytes)
-  if constexpr (sizeof(TOut) == 2) {
-    g.plain_store = !aligned16(out) || ldo % 8 != 0;
-    if (!g.plain_store && !make_out_map(&maps.out, out, T, N, ldo)) return MUSE_ERR_CUDA;
-  }
-  if (N >= T) g.m_group = static_cast<int>(std::max<int64_t>(1, (int64_t(32) << 20) / (g.m_step * K)));
-  const int pairs = std::min(g.num_tiles, sm_count() / 2);
-  if (mt == 2) MUSE_CK((launch_int8_pair<TOut, EPI, 2>(maps, g, pairs, after_quantiser, st)));
-  else MUSE_CK((launch_int8_pair<TOut, EPI, 1>(maps, g, pairs, after_quantiser, st)));
-  return MUSE_OK;
-}
-
-template <int NT, bool FUSED, typename TX, typename TOut>
-muse_status launch_int8_stream(Int8StreamArgs& a, cudaStream_t st) {
-  using S = Int8Stream<NT, FUSED>;
-  auto kern = k_int8_stream<NT, FUSED, TX, TOut>;
-  constexpr size_t kSmem = 227 * 1024 - 2 * 1024;  // less the static shared memory
-  const size_t fixed = S::kRedBytes + (FUSED ? align_up(a.T * S::xstride(a.K), 128) : 0);
-  const uint32_t stage = S::stage_bytes(a.T);
-  a.stages = static_cast<int>(std::min<size_t>(kFewMaxStages, (kSmem - fixed) / stage));
-  const size_t smem = fixed + a.stages * static_cast<size_t>(stage);
-  MUSE_CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-  Int8Launch l(dim3(std::min(a.N, sm_count())), S::kThreads, smem, st, a.after_quantiser);
-  MUSE_CK(cudaLaunchKernelEx(&l.cfg, kern, static_cast<const Int8StreamArgs&>(a)));
-  return MUSE_OK;
-}
-
-// x: codes with their scales xs, or float rows ldx apart (xs null) that the product quantises
-Int8StreamArgs int8_stream_args(const void* x, int64_t ldx, const float* xs, int64_t T, int64_t K,
-                                const muse_int8_weight& w, int64_t N, void* out, int64_t ldo, uint32_t* status,
-                                bool after_quantiser) {
-  return {x, ldx, xs, static_cast<const int8_t*>(w.codes), w.scales, out, ldo, static_cast<int>(T),
-          static_cast<int>(K), static_cast<int>(N), 0, after_quantiser, status};
-}
-
-// after_quantiser: the codes' quantiser was launched just before on the stream
-template <typename TOut>
-muse_status int8_product(const void* xc, const float* xs, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
-                         void* out, int64_t ldo, uint32_t* status, bool after_quantiser, cudaStream_t st) {
-  if (T > kInt8StreamRows) return int8_gemm<TOut>(xc, xs, T, K, w, N, out, ldo, status, after_quantiser, st);
-  Int8StreamArgs a = int8_stream_args(xc, K, xs, T, K, w, N, out, ldo, status, after_quantiser);
-  return T <= 8 ? launch_int8_stream<1, false, float, TOut>(a, st) : launch_int8_stream<2, false, float, TOut>(a, st);
-}
-muse_status int8_product(const void* xc, const float* xs, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
-                         void* out, int32_t out_dtype, int64_t ldo, uint32_t* status, bool after_quantiser,
-                         cudaStream_t st) {
-  return out_dtype == MUSE_BF16
-             ? int8_product<__nv_bfloat16>(xc, xs, T, K, w, N, out, ldo, status, after_quantiser, st)
-             : int8_product<float>(xc, xs, T, K, w, N, out, ldo, status, after_quantiser, st);
-}
-
-// float rows that the product can quantise itself: few and short enough for its registers
-bool int8_fused(const void* x, int32_t dtype, int64_t T, int64_t K, int64_t ldx) {
-  return T <= 8 && K <= int8_fused_depth(static_cast<int>(T)) && aligned16(x) &&
-         (T == 1 || ldx * static_cast<int64_t>(dtype_size(dtype)) % 16 == 0);
-}
-
-template <typename TX>
-muse_status int8_linear_fused(const void* x, int64_t ldx, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
-                              void* out, int32_t out_dtype, int64_t ldo, uint32_t* status, cudaStream_t st) {
-  Int8StreamArgs a = int8_stream_args(x, ldx, nullptr, T, K, w, N, out, ldo, status, false);
-  return out_dtype == MUSE_BF16 ? launch_int8_stream<1, true, TX, __nv_bfloat16>(a, st)
-                                : launch_int8_stream<1, true, TX, float>(a, st);
-}
-
 // the sizes, weights and output of an int8 product
 muse_status validate_int8(int64_t T, int64_t K, const muse_int8_weight* w, int64_t N, const void* out,
                           int32_t out_dtype, int64_t ldo, const uint32_t* status) {
@@ -1554,9 +1620,10 @@ muse_status muse_latent_moe_forward(const muse_moe_config* cfg, const void* x, c
                                     const void* W_pool, const void* W_gate, const void* W_up, const void* W_down,
                                     const void* gamma, const void* W_unpool, void* out, void* stream) {
   MUSE_TRY(validate_sizes(cfg));
-  const void* ptrs[] = {x, W_router, W_pool, gamma, W_unpool, out};
+  const void* ptrs[] = {x, W_router, gamma, out};
   for (const void* p : ptrs)
     if (p == nullptr || !aligned16(p)) return MUSE_ERR_INVALID_ARG;
+  if (!valid_projection(*cfg, W_pool) || !valid_projection(*cfg, W_unpool)) return MUSE_ERR_INVALID_ARG;
   MUSE_TRY(validate_experts(cfg, W_gate, W_up, W_down));
   MUSE_TRY(validate_options(cfg));
   const Layout lay = make_layout(*cfg);
@@ -1573,10 +1640,10 @@ muse_status muse_latent_moe_forward_checked(const muse_moe_config* cfg, const mu
                                             const muse_tensor* W_down, const muse_tensor* gamma,
                                             const muse_tensor* W_unpool, const muse_tensor* out, void* stream) {
   MUSE_TRY(validate_sizes(cfg));
-  ExpertOperands e;
+  WeightOperands e;
   MUSE_TRY(check_tensors(*cfg, x, W_router, W_pool, W_gate, W_up, W_down, gamma, W_unpool, out, &e));
-  return muse_latent_moe_forward(cfg, x->data, W_router->data, W_pool->data, e.gate, e.up, e.down, gamma->data,
-                                 W_unpool->data, const_cast<void*>(out->data), stream);
+  return muse_latent_moe_forward(cfg, x->data, W_router->data, e.pool, e.gate, e.up, e.down, gamma->data, e.unpool,
+                                 const_cast<void*>(out->data), stream);
 }
 
 muse_status muse_ep_workspace_layout(const muse_moe_config* cfg, int32_t ep_size, int32_t role, int64_t rows,
@@ -1600,9 +1667,10 @@ muse_status muse_ep_dispatch(const muse_moe_config* cfg, int32_t ep_size, const 
                              const void* W_pool, void* send_z, int32_t* send_expert, int32_t* rank_counts,
                              void* stream) {
   MUSE_TRY(validate_ep(cfg, ep_size));
-  const void* ptrs[] = {x, W_router, W_pool, send_z};
+  const void* ptrs[] = {x, W_router, send_z};
   for (const void* p : ptrs)
     if (p == nullptr || !aligned16(p)) return MUSE_ERR_INVALID_ARG;
+  if (!valid_projection(*cfg, W_pool)) return MUSE_ERR_INVALID_ARG;
   if (send_expert == nullptr || rank_counts == nullptr || (reinterpret_cast<uintptr_t>(send_expert) & 3u) ||
       (reinterpret_cast<uintptr_t>(rank_counts) & 3u))
     return MUSE_ERR_INVALID_ARG;
@@ -1641,9 +1709,10 @@ muse_status muse_ep_experts(const muse_moe_config* cfg, int32_t ep_size, int64_t
 muse_status muse_ep_combine(const muse_moe_config* cfg, int32_t ep_size, const void* x, const void* back_y,
                             const float* back_ss, const void* gamma, const void* W_unpool, void* out, void* stream) {
   MUSE_TRY(validate_ep(cfg, ep_size));
-  const void* ptrs[] = {x, back_y, back_ss, gamma, W_unpool, out};
+  const void* ptrs[] = {x, back_y, back_ss, gamma, out};
   for (const void* p : ptrs)
     if (p == nullptr || !aligned16(p)) return MUSE_ERR_INVALID_ARG;
+  if (!valid_projection(*cfg, W_unpool)) return MUSE_ERR_INVALID_ARG;
   MUSE_TRY(validate_options(cfg));
   const Layout lay = make_layout(*cfg, Role::kHome);
   MUSE_TRY(check_workspace(cfg, lay));
@@ -1846,10 +1915,10 @@ muse_status muse_latent_moe_few_tokens_checked(const muse_moe_config* cfg, const
                                                const muse_tensor* W_down, const muse_tensor* gamma,
                                                const muse_tensor* W_unpool, const muse_tensor* out, void* stream) {
   MUSE_TRY(validate_few(cfg));
-  ExpertOperands e;
+  WeightOperands e;
   MUSE_TRY(check_tensors(*cfg, x, W_router, W_pool, W_gate, W_up, W_down, gamma, W_unpool, out, &e));
-  return muse_latent_moe_few_tokens(cfg, x->data, W_router->data, W_pool->data, e.gate, e.up, e.down, gamma->data,
-                                    W_unpool->data, const_cast<void*>(out->data), stream);
+  return muse_latent_moe_few_tokens(cfg, x->data, W_router->data, e.pool, e.gate, e.up, e.down, gamma->data, e.unpool,
+                                    const_cast<void*>(out->data), stream);
 }
 
 muse_status muse_latent_moe_few_tokens_status(const muse_moe_config* cfg, void* stream, uint32_t* detail) {
@@ -1902,6 +1971,8 @@ const char* muse_latent_moe_stage_name(const muse_moe_config* cfg, int32_t i) {
   names[n++] = "expert_hist";
   names[n++] = "tiles";
   names[n++] = "assign_rows";
+  const bool int8 = c.proj_weights == MUSE_PROJ_INT8;
+  if (int8) names[n++] = "quant_x";
   names[n++] = "pooler";
   if (c.pre_norm_gain != nullptr) names[n++] = "pre_expert_norm";
   if (w4a4(c)) {
@@ -1914,6 +1985,7 @@ const char* muse_latent_moe_stage_name(const muse_moe_config* cfg, int32_t i) {
   if (w4a4(c)) names[n++] = "quant_h";
   names[n++] = "down_sumsq";
   names[n++] = "norm_combine";
+  if (int8) names[n++] = "quant_c";
   names[n++] = "unpooler";
   if (c.ffn_post_gain != nullptr || c.residual_gate != nullptr) names[n++] = "ffn_post_norm_gate";
   return i < n ? names[i] : nullptr;

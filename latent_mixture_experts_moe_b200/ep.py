@@ -25,7 +25,7 @@ from __future__ import annotations
 from typing import Dict, List, Optional, Sequence, Tuple
 
 from . import (EP_EXPERTS, EP_HOME, _ptr, block_config, ep_combine, ep_dispatch, ep_experts, ep_workspace_layout,
-               expert_operands, expert_weight_dims)
+               expert_operands, expert_weight_dims, projection_operand)
 
 
 class ExpertShard:
@@ -51,6 +51,8 @@ class ExpertShard:
         if lead != self.E_loc:
             raise ValueError(f"expert tensors hold {lead} experts, this rank owns {self.E_loc}")
         self.w = dict(weights)
+        for name in ("W_pool", "W_unpool"):
+            self.w[name], _ = projection_operand(weights, name)
         self.experts_args = expert_operands(weights, self.nvfp4)
         self.rank, self.G, self.T_max, self.k = ep_rank, ep_size, T_max, k
         self.dtype = {torch.float32: "f32", torch.bfloat16: "bf16"}[weights["W_router"].dtype]
