@@ -56,6 +56,7 @@ constexpr int kFewAssign = 8 * 32;    // most (token, expert) pairs: top_k <= 32
 constexpr int kFewGridMax = 192;      // CTAs a workspace has partial sums for
 constexpr int kFewProducers = 4;      // producer warps: one for activations, the others for weights
 constexpr int kFewStore = 4;          // store warps
+constexpr int kFewPer = 8 / kFewStore;  // tokens of each
 constexpr int kFewWarps = 8;          // product warps
 constexpr int kFewThreads = 32 * (kFewProducers + kFewStore + kFewWarps);
 constexpr int kFewRows = 32;          // weight rows of a stage (gate/up: 16 features of each)
@@ -592,6 +593,16 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
+// (zeros and no access where off)
+__device__ __forceinline__ uint4 lds128_if(bool on, uint32_t a) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+      "mov.b32 %3, 0;\n\t@p ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "r"(a), "r"(static_cast<uint32_t>(on)));
+  return v;
+}
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
   uint16_t v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
@@ -624,7 +635,9 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int
                                             volatile int* abort, FewRed& out) {
   using G = FewGeo<FORMAT>;
   const int g = lane >> 2, t = lane & 3;
-  const int gx = min(g, n - 1);  // token rows past n are not staged (their columns are not used)
+  // token rows past n are not staged, and their columns not used; reading none for them saves up
+  // to three quarters of the activations' shared-memory cycles (NVFP4, eight tokens: 440 -> 425 us)
+  const bool has_x = g < n;
   float acc[8];          // float32: this lane's row, 8 tokens
   float chain[2][2][4];  // MMA: two 16-row tiles, each in two sums, so that fewer MMAs wait for one another
 #pragma unroll
@@ -641,12 +654,12 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int
     __syncwarp();
     const uint32_t st = ring.addr();
     if constexpr (FORMAT == FEW_BF16) {
-      const uint32_t w = st + g * G::wstride + t * 16u, x = st + G::xoff + gx * xstride + t * 16u;
+      const uint32_t w = st + g * G::wstride + t * 16u, x = st + G::xoff + g * xstride + t * 16u;
       const uint32_t r8 = 8u * G::wstride;
 #pragma unroll 2
       for (int s = wc; s < kn / 32; s += kFewWarps) {  // 32 elements = 64 bytes of each row
         const uint32_t o = 64u * s;
-        const uint4 b = lds128(x + o), a0 = lds128(w + o), a1 = lds128(w + r8 + o), a2 = lds128(w + 2 * r8 + o),
+        const uint4 b = lds128_if(has_x, x + o), a0 = lds128(w + o), a1 = lds128(w + r8 + o), a2 = lds128(w + 2 * r8 + o),
                     a3 = lds128(w + 3 * r8 + o);
         mma_bf16_16816(chain[0][0], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
         mma_bf16_16816(chain[0][1], a2.x, a3.x, a2.y, a3.y, b.x, b.y);
@@ -654,9 +667,9 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int
         mma_bf16_16816(chain[1][1], a2.z, a3.z, a2.w, a3.w, b.z, b.w);
       }
     } else if constexpr (FORMAT == FEW_NVFP4) {
-      const uint32_t w = st + g * G::wstride + t * 16u, x = st + G::xoff + gx * xstride + t * 64u + (t >> 1) * 16u;
+      const uint32_t w = st + g * G::wstride + t * 16u, x = st + G::xoff + g * xstride + t * 64u + (t >> 1) * 16u;
       const uint32_t sc = st + G::soff + g * G::sstride + t * 2u;
-#pragma unroll 2
+#pragma unroll 1
       for (int s = wc; s < kn / 128; s += kFewWarps) {  // 128 elements; this lane's two blocks: 2 t, 2 t + 1
         uint4 cw[4];
         uint32_t sw[4];
@@ -668,7 +681,7 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int
         // 16 MMAs in four chains (block h, row tile m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // the lane's blocks: two code words a row each
-          const uint4 x0 = lds128(x + 288u * s + 32u * h), x1 = lds128(x + 288u * s + 32u * h + 16u);
+          const uint4 x0 = lds128_if(has_x, x + 288u * s + 32u * h), x1 = lds128_if(has_x, x + 288u * s + 32u * h + 16u);
           const uint32_t xw[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
@@ -914,14 +927,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_cons
     });
     arrive(FEW_H);
     {
-      // sums of squares of the rows this CTA computes of each position: tokens ws and ws + 4 of
-      // the current expert
-      float ss[2] = {0.0f, 0.0f};
+      // sums of squares of the rows this CTA computes of each position: tokens ws, ws + kFewStore, ...
+      // of the current expert
+      float ss[kFewPer] = {};
       int ss_d = -1;
       auto flush = [&]() {
         if (ss_d < 0) return;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kFewPer; ++h) {
           const int pos = route.first[ss_d] + ws + kFewStore * h;
           if (lane == 0 && pos < route.first[ss_d + 1]) p.ss[static_cast<int64_t>(pos) * kFewGridMax + blockIdx.x] = ss[h];
           ss[h] = 0.0f;
@@ -940,13 +953,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_cons
             u *= 1.0f + to_f32(gamma[(p.gamma_shared ? 0 : static_cast<int64_t>(e) * L) + c.f + lane]);
         }
         const float s = warp_sum(u * u);
-        if (j < kFewStore) ss[0] += s;
-        else ss[1] += s;
+#pragma unroll
+        for (int h = 0; h < kFewPer; ++h) ss[h] += j / kFewStore == h ? s : 0.0f;
       });
       flush();
       arrive(FEW_Y);
     }
-    float ssf[2] = {0.0f, 0.0f};  // of this CTA's rows of tokens ws and ws + 4
+    float ssf[kFewPer] = {};  // of this CTA's rows of tokens ws, ws + kFewStore, ...
     each(FEW_OUT, [&](const FewChunks& c, int j, float v) {
       const int64_t o = static_cast<int64_t>(j) * D + c.f + lane;
       if (!finish) {
@@ -959,12 +972,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_cons
         if (post != nullptr) u = v * (1.0f + to_f32(post[c.f + lane]));
       }
       const float s = warp_sum(u * u);
-      if (j < kFewStore) ssf[0] += s;
-      else ssf[1] += s;
+#pragma unroll
+      for (int h = 0; h < kFewPer; ++h) ssf[h] += j / kFewStore == h ? s : 0.0f;
     });
     if (finish) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < kFewPer; ++h)
         if (lane == 0 && ws + kFewStore * h < T) p.ssf[(ws + kFewStore * h) * kFewGridMax + blockIdx.x] = ssf[h];
       arrive(FEW_F);
     }
