@@ -65,49 +65,57 @@ constexpr int kFewBarriers = 8;       // grid barriers of a call, their counters
 constexpr uint32_t kFewRedFloats = kFewWarps * 8u * 33u;      // partial sums of a chunk
 constexpr uint32_t kFewRedBytes = 2u * kFewRedFloats * 4u;    // two chunks'
 
-enum FewFormat : int { FEW_BF16 = 0, FEW_NVFP4 = 1, FEW_F32 = 2 };
+enum FewFormat : int { FEW_BF16 = 0, FEW_NVFP4 = 1, FEW_F32 = 2, FEW_BF16_SHORT = 3 };
 
 // How the stages of a product with weights of a format lie in shared memory: at most kc elements
 // of K per stage, so that every product warp has a share of each (its unit: 32 bf16 elements,
 // 128 NVFP4, 4 float32); weight rows wstride bytes apart from offset 0, NVFP4 block scales
-// sstride apart from soff, activation rows xstride(n) apart from xoff. 2048 elements of NVFP4
-// rows are as many bytes as 512 of bf16, but each activation row then takes 4 KB: with more
-// than two tokens on an expert (rare) its stages hold less of K instead of more bytes.
+// sstride apart from soff, activation rows xstride apart from xoff.
+// 2048 elements of NVFP4 rows are as many bytes as 512 of bf16, but each activation row would
+// take 4 KB of every stage, most of a stage's time with several tokens on an expert: where they
+// fit (FewArgs::x_bytes), an expert's activation rows lie whole in a buffer of their own, copied
+// once for all of a CTA's rows of that expert (16 experts with four tokens each: 390 us without);
+// otherwise its stages hold less of K (depth).
+// FEW_BF16_SHORT: the dense products beside NVFP4 experts, whose ring is shorter by that buffer.
 // The row distances keep the product warps' reads free of bank conflicts: bf16 rows 64 bytes
 // past a multiple of 128 (a quarter warp reads 64 bytes of two rows), and codes too, float rows
 // 16 past it (eight lanes read one row each), scales an odd multiple of 16; f16 activations
 // beside codes, of which a lane reads 64 bytes in four steps, have 16 spare bytes after every
-// 128 and rows 32 past a multiple of 128.
+// 128 and rows 32 (or 96) past a multiple of 128.
 template <int FORMAT>
 struct FewGeo {
-  static constexpr int kc = FORMAT == FEW_NVFP4 ? 2048 : FORMAT == FEW_BF16 ? 512 : 256;
+  static constexpr int kc = FORMAT == FEW_NVFP4 ? 2048 : FORMAT == FEW_BF16 ? 512 : FORMAT == FEW_BF16_SHORT ? 384 : 256;
   static constexpr int act_size = FORMAT == FEW_F32 ? 4 : 2;
   static constexpr uint32_t row_bytes = FORMAT == FEW_NVFP4 ? kc / 2 : kc * act_size;
   static constexpr uint32_t wstride = row_bytes + (FORMAT == FEW_F32 ? 16 : 64);
   static constexpr uint32_t soff = kFewRows * wstride;
   static constexpr uint32_t sstride = FORMAT == FEW_NVFP4 ? (kc / 16) | 16 : 0;
   static constexpr uint32_t xoff = soff + kFewRows * sstride;
-  // elements of K per stage, and the distance of activation rows, with n tokens
-  __host__ __device__ static constexpr int depth(int n) {
-    return FORMAT != FEW_NVFP4 || n <= 2 ? kc : n <= 4 ? kc / 2 : kc / 4;
+  // elements of K per stage with n tokens; whole: the activations have their own buffer
+  __host__ __device__ static constexpr int depth(int n, bool whole) {
+    return FORMAT != FEW_NVFP4 || whole || n <= 2 ? kc : n <= 4 ? kc / 2 : kc / 4;
   }
-  __host__ __device__ static constexpr uint32_t xstride(int n) {
-    return static_cast<uint32_t>(FORMAT == FEW_NVFP4 ? depth(n) / 8 * 9 * act_size + 32
-                                                     : depth(n) * act_size + (FORMAT == FEW_BF16 ? 64 : 16));
+  // distance of activation rows that hold k elements
+  __host__ __device__ static constexpr uint32_t xstride(int k) {
+    return static_cast<uint32_t>(FORMAT == FEW_NVFP4 ? k / 8 * 9 * act_size + 32
+                                                     : k * act_size + (FORMAT == FEW_F32 ? 16 : 64));
   }
-  // where byte a of an activation row's piece lies
+  // where byte a of an activation row lies
   __device__ static constexpr uint32_t xbyte(uint32_t a) { return FORMAT == FEW_NVFP4 ? a + a / 128 * 16 : a; }
   // bytes of a stage that holds up to T tokens
-  static constexpr uint32_t bytes(int T) {
+  static constexpr uint32_t bytes(int T, bool whole) {
     uint32_t x = 0;
-    for (int n = 1; n <= T; ++n) x = n * xstride(n) > x ? n * xstride(n) : x;
+    for (int n = 1; n <= T && !(FORMAT == FEW_NVFP4 && whole); ++n)
+      x = n * xstride(depth(n, false)) > x ? n * xstride(depth(n, false)) : x;
     return xoff + x;
   }
 };
+constexpr uint32_t kFewXBytes = 74 * 1024;  // most that an expert's activation rows may take: 8 rows of 4096
 
 struct FewArgs {
   int stages;             // ring depth
   uint32_t stage_bytes;
+  uint32_t x_bytes;       // NVFP4 experts: buffer of an expert's activation rows (0: in the stages)
   int T, D, L, I, E, k;
   int router_mode, norm_mode, gamma_shared;
   float eps, logit_scale, rsf, pre_norm_eps, ffn_pre_eps, ffn_post_eps, inv_temp, gate_eps;
@@ -483,44 +491,65 @@ struct FewSource {
   }
 };
 
+// The buffer of an expert's activation rows: filled by producer warp 0 once the product warps are
+// done with the expert before (barrier `free`); its copies precede that warp's arrival at the
+// expert's first stage, which therefore also says that the rows are there.
+struct FewX {
+  uint32_t base, free;
+  uint32_t phase;  // of the next wait on / arrival at free
+};
+
 // One producer warp's copies of a job: warp 0 the activations, once
 // `ready` (the barrier before this phase; nullptr: nothing to wait for) has passed; the others
 // each every third weight row (and a third of the block scales), as far ahead as the ring is free. A stage's addresses advance by
 // constants from those of the chunk, so that a copy costs a few instructions.
 template <typename TA, int FORMAT>
-__device__ __forceinline__ void few_produce(const FewSource<TA, FORMAT>& q, FewRing& ring, const uint32_t* ready,
-                                            volatile int* abort, int pw, int lane) {
+__device__ __forceinline__ void few_produce(const FewSource<TA, FORMAT>& q, FewRing& ring, FewX& xbuf,
+                                            const uint32_t* ready, volatile int* abort, int pw, int lane) {
   using G = FewGeo<FORMAT>;
   constexpr int kWeightWarps = kFewProducers - 1;
   constexpr int kMine = (kFewRows + kWeightWarps - 1) / kWeightWarps;
   const FewArgs& p = q.p;
   const int K = q.job.K;
   FewChunks c(q.job.U, q.job.group, q.job.most);
+  int expert = -1;  // whose rows the buffer holds
   if (pw == 0 && ready != nullptr) {
     if (lane == 0) few_poll(ready, gridDim.x, abort, p.status, 0xB00u + q.job.phase);
     __syncwarp();
   }
   for (; !c.done(); c.next()) {
-    const int n = q.tokens(c), kc = G::depth(n);
+    const bool whole = FORMAT == FEW_NVFP4 && p.x_bytes > 0;
+    const int n = q.tokens(c), kc = G::depth(n, whole);
     if (pw == 0) {
-      const uint32_t xstride = G::xstride(n);
+      const uint32_t xstride = G::xstride(whole ? K : kc);
       const uint8_t* x = q.activation(c, min(lane, n - 1));  // lane j: token j's row
+      // `bytes` of every row to dst
+      auto rows = [&](uint32_t dst, int bytes) {
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+          const uint8_t* xj = reinterpret_cast<const uint8_t*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x), j));
+#pragma unroll 2
+          for (int a = 16 * lane; a - 16 * lane < bytes; a += 512)
+            cp_async16_if(a < bytes, dst + xstride * j + G::xbyte(a), xj + a);
+        }
+      };
+      if (whole && c.d != expert) {
+        expert = c.d;
+        if (few_mbar_wait(xbuf.free, xbuf.phase ^ 1u, abort, p.status, 0xA80u)) {
+          __syncwarp();
+          rows(xbuf.base, K * G::act_size);
+        }
+        xbuf.phase ^= 1u;
+        __syncwarp();
+      }
 #pragma unroll 1
       for (int k0 = 0; k0 < K; k0 += kc) {
         const int kn = min(kc, K - k0);
         // (a wait that gave up: no copies; the arrivals go on so that nobody waits for them)
         const bool ok = few_mbar_wait(ring.empty(), ring.phase ^ 1u, abort, p.status, 0xA00u + ring.stage);
         if (__all_sync(0xffffffffu, ok)) {
-          const uint32_t st = ring.addr();
-          const int bytes = kn * G::act_size;
-#pragma unroll 1
-          for (int j = 0; j < n; ++j) {
-            const uint8_t* xj = reinterpret_cast<const uint8_t*>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x), j));
-            const uint32_t dst = st + G::xoff + xstride * j;
-#pragma unroll 2
-            for (int a = 16 * lane; a - 16 * lane < bytes; a += 512) cp_async16_if(a < bytes, dst + G::xbyte(a), xj + a);
-          }
+          if (!whole) rows(ring.addr() + G::xoff, kn * G::act_size);
         }
         cp_async_arrive(ring.full());
         ring.next();
@@ -631,8 +660,8 @@ struct FewRed {
 // One chunk's products: the stages of 32 weight rows and n activation rows, this warp's share
 // of K; the warp's sums go to the next buffer of partial sums.
 template <int FORMAT>
-__device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int K, int n, int wc, int lane,
-                                            volatile int* abort, FewRed& out) {
+__device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, const FewX& xbuf, int K, int n, int wc,
+                                            int lane, volatile int* abort, FewRed& out) {
   using G = FewGeo<FORMAT>;
   const int g = lane >> 2, t = lane & 3;
   // token rows past n are not staged, and their columns not used; reading none for them saves up
@@ -645,15 +674,16 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int
     acc[i] = 0.0f;
     chain[0][i >> 2][i & 3] = chain[1][i >> 2][i & 3] = 0.0f;
   }
-  const int kc = G::depth(n);
-  const uint32_t xstride = G::xstride(n);
+  const bool whole = FORMAT == FEW_NVFP4 && p.x_bytes > 0;
+  const int kc = G::depth(n, whole);
+  const uint32_t xstride = G::xstride(whole ? K : kc);
 #pragma unroll 1
   for (int k0 = 0; k0 < K; k0 += kc) {
     const int kn = min(kc, K - k0);
     few_mbar_wait(ring.full(), ring.phase, abort, p.status, 0xC00u + ring.stage);
     __syncwarp();
     const uint32_t st = ring.addr();
-    if constexpr (FORMAT == FEW_BF16) {
+    if constexpr (FORMAT == FEW_BF16 || FORMAT == FEW_BF16_SHORT) {
       const uint32_t w = st + g * G::wstride + t * 16u, x = st + G::xoff + g * xstride + t * 16u;
       const uint32_t r8 = 8u * G::wstride;
 #pragma unroll 2
@@ -667,7 +697,8 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, int
         mma_bf16_16816(chain[1][1], a2.z, a3.z, a2.w, a3.w, b.z, b.w);
       }
     } else if constexpr (FORMAT == FEW_NVFP4) {
-      const uint32_t w = st + g * G::wstride + t * 16u, x = st + G::xoff + g * xstride + t * 64u + (t >> 1) * 16u;
+      const uint32_t w = st + g * G::wstride + t * 16u;
+      const uint32_t x = (whole ? xbuf.base + k0 / 8 * 18 : st + G::xoff) + g * xstride + t * 64u + (t >> 1) * 16u;
       const uint32_t sc = st + G::soff + g * G::sstride + t * 2u;
 #pragma unroll 1
       for (int s = wc; s < kn / 128; s += kFewWarps) {  // 128 elements; this lane's two blocks: 2 t, 2 t + 1
@@ -809,18 +840,19 @@ enum FewBarrier : int { FEW_XN = 0, FEW_LOGITS, FEW_Z, FEW_ZN, FEW_H, FEW_Y, FEW
 template <typename TA, bool FP4>
 __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_constant__ FewArgs p) {
   using TZ = typename FewTypes<TA, FP4>::Z;
-  constexpr int DENSE = sizeof(TA) == 4 ? FEW_F32 : FEW_BF16;
+  constexpr int DENSE = sizeof(TA) == 4 ? FEW_F32 : FP4 ? FEW_BF16_SHORT : FEW_BF16;
   constexpr int EXPERT = FP4 ? FEW_NVFP4 : DENSE;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];  // partial sums, activation rows, the ring
   __shared__ FewRoute route;
-  __shared__ __align__(8) uint64_t bars[2 * kFewMaxStages + 4];
+  __shared__ __align__(8) uint64_t bars[2 * kFewMaxStages + 5];
   __shared__ float part[32];
   __shared__ float scale_s[kFewAssign];
   __shared__ int abort_flag;
   volatile int* abort = &abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int T = p.T, D = p.D, L = p.L, I = p.I, E = p.E;
-  FewRing ring{smem_u32(bars), smem_u32(smem) + kFewRedBytes, p.stages, 0, 0u, p.stage_bytes};
+  FewRing ring{smem_u32(bars), smem_u32(smem) + kFewRedBytes + p.x_bytes, p.stages, 0, 0u, p.stage_bytes};
+  FewX xbuf{smem_u32(smem) + kFewRedBytes, smem_u32(bars + 2 * kFewMaxStages + 4), 0u};
   FewRed red{smem_u32(bars + 2 * kFewMaxStages), reinterpret_cast<float*>(smem), 0, 0u};
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -831,6 +863,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_cons
       mbar_init(red.bar0 + 8u * i, kFewWarps);
       mbar_init(red.bar0 + 16u + 8u * i, kFewStore);
     }
+    mbar_init(xbuf.free, kFewWarps);
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -851,9 +884,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_cons
       const uint32_t* ready = ph <= FEW_POOL ? (pre ? counter(FEW_XN) : nullptr)
                               : counter(ph == FEW_GATE_UP ? (zn ? FEW_ZN : FEW_Z) : ph == FEW_DOWN ? FEW_H : FEW_C);
       if (FP4 && (ph == FEW_GATE_UP || ph == FEW_DOWN))
-        few_produce(FewSource<TA, EXPERT>{p, route, xin, job}, ring, ready, abort, warp, lane);
+        few_produce(FewSource<TA, EXPERT>{p, route, xin, job}, ring, xbuf, ready, abort, warp, lane);
       else
-        few_produce(FewSource<TA, DENSE>{p, route, xin, job}, ring, ready, abort, warp, lane);
+        few_produce(FewSource<TA, DENSE>{p, route, xin, job}, ring, xbuf, ready, abort, warp, lane);
     }
     cp_async_wait_all();  // nothing in flight when the CTA leaves, also after a wait that gave up
     return;
@@ -1024,8 +1057,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_cons
 #pragma unroll 1
     for (FewChunks c(job.U, job.group, job.most); !c.done(); c.next()) {
       const int n = experts ? route.first[c.d + 1] - route.first[c.d] : T;
-      if (FP4 && experts) few_consume<EXPERT>(p, ring, job.K, n, wc, lane, abort, red);
-      else few_consume<DENSE>(p, ring, job.K, n, wc, lane, abort, red);
+      if (FP4 && experts) few_consume<EXPERT>(p, ring, xbuf, job.K, n, wc, lane, abort, red);
+      else few_consume<DENSE>(p, ring, xbuf, job.K, n, wc, lane, abort, red);
+      // the last chunk of an expert: its activation rows may go
+      if (FP4 && experts && p.x_bytes > 0 && lane == 0 && (c.left == c.len || c.f + c.len == c.group)) mbar_arrive(xbuf.free);
     }
   }
   if (!finish) return;

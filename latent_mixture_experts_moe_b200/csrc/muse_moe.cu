@@ -1457,11 +1457,15 @@ muse_status launch_few(FewArgs& a, cudaStream_t st) {
   auto kern = k_few_tokens<TA, FP4>;
   const int grid = std::min(sm_count(), kFewGridMax);
   constexpr uint32_t kSmem = 227 * 1024 - 12 * 1024;  // less the static shared memory
-  constexpr int kDense = sizeof(TA) == 2 ? FEW_BF16 : FEW_F32;
+  constexpr int kDense = sizeof(TA) == 4 ? FEW_F32 : FP4 ? FEW_BF16_SHORT : FEW_BF16;
+  constexpr int kExpert = FP4 ? FEW_NVFP4 : kDense;
+  const uint32_t x = FP4 ? a.T * FewGeo<FEW_NVFP4>::xstride(std::max(a.L, a.I)) : 0;
+  a.x_bytes = x <= kFewXBytes ? static_cast<uint32_t>(align_up(x, 128)) : 0;
   a.stage_bytes = static_cast<uint32_t>(
-      align_up(std::max(FewGeo<kDense>::bytes(a.T), FewGeo<FP4 ? FEW_NVFP4 : kDense>::bytes(a.T)), 128));
-  a.stages = static_cast<int>(std::min<uint32_t>(kFewMaxStages, (kSmem - kFewRedBytes) / a.stage_bytes));
-  const size_t smem = kFewRedBytes + static_cast<size_t>(a.stages) * a.stage_bytes;
+      align_up(std::max(FewGeo<kDense>::bytes(a.T, false), FewGeo<kExpert>::bytes(a.T, a.x_bytes > 0)), 128));
+  const uint32_t fixed = kFewRedBytes + a.x_bytes;
+  a.stages = static_cast<int>(std::min<uint32_t>(kFewMaxStages, (kSmem - fixed) / a.stage_bytes));
+  const size_t smem = fixed + static_cast<size_t>(a.stages) * a.stage_bytes;
   void* args[] = {&a};
   MUSE_CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
   MUSE_CK(cudaMemsetAsync(a.status, 0, kFewHeader, st));
