@@ -111,11 +111,17 @@ struct FewGeo {
   }
 };
 constexpr uint32_t kFewXBytes = 74 * 1024;  // most that an expert's activation rows may take: 8 rows of 4096
+// The router's rows are few for a CTA (256 over 148): with at most kFewNarrow of them a stage
+// holds 2 or 4 times as much of K (FewArgs::narrow), or the ring would hold next to nothing (the
+// logits of the full-size layer were ready after 8.5 us, with DRAM idle, against 3).
+constexpr int kFewNarrow = 4;
+
 
 struct FewArgs {
   int stages;             // ring depth
   uint32_t stage_bytes;
   uint32_t x_bytes;       // NVFP4 experts: buffer of an expert's activation rows (0: in the stages)
+  int narrow;             // the router's stages hold this many times as much of K (0: they are as the others)
   int T, D, L, I, E, k;
   int router_mode, norm_mode, gamma_shared;
   float eps, logit_scale, rsf, pre_norm_eps, ffn_pre_eps, ffn_post_eps, inv_temp, gate_eps;
@@ -519,9 +525,10 @@ __device__ __forceinline__ void few_produce(const FewSource<TA, FORMAT>& q, FewR
   }
   for (; !c.done(); c.next()) {
     const bool whole = FORMAT == FEW_NVFP4 && p.x_bytes > 0;
-    const int n = q.tokens(c), kc = G::depth(n, whole);
+    const int narrow = q.job.phase == FEW_ROUTER && FORMAT != FEW_NVFP4 ? p.narrow : 0;
+    const int n = q.tokens(c), kc = narrow > 0 ? G::kc * narrow : G::depth(n, whole);
     if (pw == 0) {
-      const uint32_t xstride = G::xstride(whole ? K : kc);
+      const uint32_t xstride = G::xstride(whole ? K : kc), xoff = narrow > 0 ? kFewNarrow * xstride : G::xoff;
       const uint8_t* x = q.activation(c, min(lane, n - 1));  // lane j: token j's row
       // `bytes` of every row to dst
       auto rows = [&](uint32_t dst, int bytes) {
@@ -549,11 +556,28 @@ __device__ __forceinline__ void few_produce(const FewSource<TA, FORMAT>& q, FewR
         // (a wait that gave up: no copies; the arrivals go on so that nobody waits for them)
         const bool ok = few_mbar_wait(ring.empty(), ring.phase ^ 1u, abort, p.status, 0xA00u + ring.stage);
         if (__all_sync(0xffffffffu, ok)) {
-          if (!whole) rows(ring.addr() + G::xoff, kn * G::act_size);
+          if (!whole) rows(ring.addr() + xoff, kn * G::act_size);
         }
         cp_async_arrive(ring.full());
         ring.next();
         x += kc * G::act_size;
+      }
+    } else if (FORMAT != FEW_NVFP4 && narrow > 0) {
+#pragma unroll 1
+      for (int k0 = 0; k0 < K; k0 += kc) {
+        const int bytes = min(kc, K - k0) * G::act_size;
+        const bool ok = few_mbar_wait(ring.empty(), ring.phase ^ 1u, abort, p.status, 0xA00u + ring.stage);
+        if (__all_sync(0xffffffffu, ok)) {
+#pragma unroll 1
+          for (int i = pw - 1; i < c.len; i += kWeightWarps) {
+            const uint8_t* w = q.row(c, false) + i * q.row_bytes() + k0 * static_cast<int64_t>(G::act_size);
+            const uint32_t dst = ring.addr() + i * G::xstride(kc);
+#pragma unroll 4
+            for (int a = 16 * lane; a - 16 * lane < bytes; a += 512) cp_async16_if(a < bytes, dst + a, w + a);
+          }
+        }
+        cp_async_arrive(ring.full());
+        ring.next();
       }
     } else {
       // places i = pw - 1 + kWeightWarps * m; from 16 on (gate/up) of the other matrix
@@ -660,8 +684,8 @@ struct FewRed {
 // One chunk's products: the stages of 32 weight rows and n activation rows, this warp's share
 // of K; the warp's sums go to the next buffer of partial sums.
 template <int FORMAT>
-__device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, const FewX& xbuf, int K, int n, int wc,
-                                            int lane, volatile int* abort, FewRed& out) {
+__device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, const FewX& xbuf, int phase, int K, int n,
+                                            int wc, int lane, volatile int* abort, FewRed& out) {
   using G = FewGeo<FORMAT>;
   const int g = lane >> 2, t = lane & 3;
   // token rows past n are not staged, and their columns not used; reading none for them saves up
@@ -675,8 +699,12 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, con
     chain[0][i >> 2][i & 3] = chain[1][i >> 2][i & 3] = 0.0f;
   }
   const bool whole = FORMAT == FEW_NVFP4 && p.x_bytes > 0;
-  const int kc = G::depth(n, whole);
+  const int narrow = phase == FEW_ROUTER && FORMAT != FEW_NVFP4 ? p.narrow : 0;
+  const int kc = narrow > 0 ? G::kc * narrow : G::depth(n, whole);
   const uint32_t xstride = G::xstride(whole ? K : kc);
+  // a narrow stage holds kFewNarrow rows: the other rows of the MMA read these again, for nothing
+  const uint32_t wstride = narrow > 0 ? xstride : G::wstride;
+  const uint32_t xoff = narrow > 0 ? kFewNarrow * xstride : G::xoff;
 #pragma unroll 1
   for (int k0 = 0; k0 < K; k0 += kc) {
     const int kn = min(kc, K - k0);
@@ -684,8 +712,9 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, con
     __syncwarp();
     const uint32_t st = ring.addr();
     if constexpr (FORMAT == FEW_BF16 || FORMAT == FEW_BF16_SHORT) {
-      const uint32_t w = st + g * G::wstride + t * 16u, x = st + G::xoff + g * xstride + t * 16u;
-      const uint32_t r8 = 8u * G::wstride;
+      const uint32_t w = st + (narrow > 0 ? g & (kFewNarrow - 1) : g) * wstride + t * 16u;
+      const uint32_t x = st + xoff + g * xstride + t * 16u;
+      const uint32_t r8 = narrow > 0 ? 0u : 8u * wstride;
 #pragma unroll 2
       for (int s = wc; s < kn / 32; s += kFewWarps) {  // 32 elements = 64 bytes of each row
         const uint32_t o = 64u * s;
@@ -734,7 +763,8 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, con
         }
       }
     } else {
-      const uint32_t w = st + lane * G::wstride, x = st + G::xoff;
+      const uint32_t w = st + (narrow > 0 ? lane & (kFewNarrow - 1) : lane) * wstride;
+      const uint32_t x = st + xoff;
 #pragma unroll 2
       for (int s = wc; s < kn / 4; s += kFewWarps) {
         const float4 a = as_float4(lds128(w + 16u * s));
@@ -798,7 +828,8 @@ __device__ __forceinline__ void few_norm_row(const TS* src, const TG* w, TD* dst
   for (int i = tid; i < n; i += 32 * kFewWarps) dst[i] = from_f32<TD>(to_f32(src[i]) * scale * (1.0f + to_f32(w[i])));
 }
 
-// c = sum_j g_j y_j / rms_j (1 + gamma) by the product warps, each CTA a slice of it.
+// c = sum_j g_j y_j / rms_j (1 + gamma) by the product warps, each CTA a slice of it. (All of it in
+// every CTA, one grid barrier less, took 2 to 14 us more in small layers.)
 template <typename TA>
 __device__ __forceinline__ void few_combine(const FewArgs& p, const FewRoute& route, float* scale_s, int wc, int lane,
                                             int tid) {
@@ -1057,8 +1088,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_cons
 #pragma unroll 1
     for (FewChunks c(job.U, job.group, job.most); !c.done(); c.next()) {
       const int n = experts ? route.first[c.d + 1] - route.first[c.d] : T;
-      if (FP4 && experts) few_consume<EXPERT>(p, ring, xbuf, job.K, n, wc, lane, abort, red);
-      else few_consume<DENSE>(p, ring, xbuf, job.K, n, wc, lane, abort, red);
+      if (FP4 && experts) few_consume<EXPERT>(p, ring, xbuf, ph, job.K, n, wc, lane, abort, red);
+      else few_consume<DENSE>(p, ring, xbuf, ph, job.K, n, wc, lane, abort, red);
       // the last chunk of an expert: its activation rows may go
       if (FP4 && experts && p.x_bytes > 0 && lane == 0 && (c.left == c.len || c.f + c.len == c.group)) mbar_arrive(xbuf.free);
     }

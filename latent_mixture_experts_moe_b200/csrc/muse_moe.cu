@@ -1463,6 +1463,10 @@ muse_status launch_few(FewArgs& a, cudaStream_t st) {
   a.x_bytes = x <= kFewXBytes ? static_cast<uint32_t>(align_up(x, 128)) : 0;
   a.stage_bytes = static_cast<uint32_t>(
       align_up(std::max(FewGeo<kDense>::bytes(a.T, false), FewGeo<kExpert>::bytes(a.T, a.x_bytes > 0)), 128));
+  a.narrow = 0;
+  if (cdiv(a.E, grid) <= kFewNarrow)
+    for (int f = 2; f <= 4 && (kFewNarrow + a.T) * FewGeo<kDense>::xstride(f * FewGeo<kDense>::kc) <= a.stage_bytes; f *= 2)
+      a.narrow = f;
   const uint32_t fixed = kFewRedBytes + a.x_bytes;
   a.stages = static_cast<int>(std::min<uint32_t>(kFewMaxStages, (kSmem - fixed) / a.stage_bytes));
   const size_t smem = fixed + static_cast<size_t>(a.stages) * a.stage_bytes;
