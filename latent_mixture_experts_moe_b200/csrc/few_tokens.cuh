@@ -60,7 +60,9 @@ constexpr int kFewPer = 8 / kFewStore;  // tokens of each
 constexpr int kFewWarps = 8;          // product warps
 constexpr int kFewThreads = 32 * (kFewProducers + kFewStore + kFewWarps);
 constexpr int kFewRows = 32;          // weight rows of a stage (gate/up: 16 features of each)
-constexpr int kFewMaxStages = 16;
+// More stages than 4 only lengthen the memory system's queues, and with them every barrier's
+// round trips (one token, full-size bf16 layer: 165 us with 3 or 5 stages, 159 with 4).
+constexpr int kFewMaxStages = 4;
 constexpr int kFewBarriers = 8;       // grid barriers of a call, their counters 128 bytes apart
 constexpr uint32_t kFewRedFloats = kFewWarps * 8u * 33u;      // partial sums of a chunk
 constexpr uint32_t kFewRedBytes = 2u * kFewRedFloats * 4u;    // two chunks'

@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(256, 5) k_quant_rows_int8(const T* __restrict_
 // Bound by reading the weights: one row through 4096 x 8192 weights in 6.0 us (5.6 TB/s). From 17
 // rows on the split-K kernel is faster (64 rows: 10 us, against 27 here: every SM fetches all rows).
 constexpr int kInt8StreamRows = 16;
+constexpr int kInt8MaxStages = kFewMaxStages;  // (the ring's barriers are laid out for as many)
 template <int NT, bool FUSED>
 struct Int8Stream {
   static constexpr int R = 32;                        // weight rows of a stage
@@ -203,7 +204,7 @@ template <int NT, bool FUSED, typename TX, typename TOut>
 __global__ void __launch_bounds__(Int8Stream<NT, FUSED>::kThreads, 1) k_int8_stream(const Int8StreamArgs p) {
   using S = Int8Stream<NT, FUSED>;
   extern __shared__ __align__(128) uint8_t smem[];  // partial sums, quantised rows (fused), the ring
-  __shared__ __align__(8) uint64_t bars[2 * kFewMaxStages];
+  __shared__ __align__(8) uint64_t bars[2 * kInt8MaxStages];
   __shared__ uint32_t part[8];
   __shared__ float xs[8 * NT];
   __shared__ int abort_flag;
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(Int8Stream<NT, FUSED>::kThreads, 1) k_int8_str
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(smem_u32(bars + i), 128);
-      mbar_init(smem_u32(bars + kFewMaxStages + i), 8);
+      mbar_init(smem_u32(bars + kInt8MaxStages + i), 8);
     }
     abort_flag = 0;
     fence_mbar_init();

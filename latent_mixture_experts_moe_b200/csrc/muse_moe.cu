@@ -710,7 +710,7 @@ muse_status launch_int8_stream(Int8StreamArgs& a, cudaStream_t st) {
   constexpr size_t kSmem = 227 * 1024 - 2 * 1024;  // less the static shared memory
   const size_t fixed = S::kRedBytes + (FUSED ? align_up(a.T * S::xstride(a.K), 128) : 0);
   const uint32_t stage = S::stage_bytes(a.T);
-  a.stages = static_cast<int>(std::min<size_t>(kFewMaxStages, (kSmem - fixed) / stage));
+  a.stages = static_cast<int>(std::min<size_t>(kInt8MaxStages, (kSmem - fixed) / stage));
   const size_t smem = fixed + a.stages * static_cast<size_t>(stage);
   MUSE_CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
   Int8Launch l(dim3(std::min(a.N, sm_count())), S::kThreads, smem, st, a.after_quantiser);
