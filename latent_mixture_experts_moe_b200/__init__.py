@@ -394,13 +394,14 @@ def quantize_nvfp4_rows(src, codes, scales, stream=None) -> None:
 def _rows(t, name: str):
     """Pointer, muse_dtype and row distance of a 2-D float tensor whose rows are contiguous."""
     import torch
-    if t.dim() != 2 or t.dtype not in (torch.float32, torch.bfloat16):
+    dtype = MUSE_BF16 if t.dtype is torch.bfloat16 else MUSE_F32 if t.dtype is torch.float32 else -1
+    if dtype < 0 or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D float32 or bfloat16 tensor")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    step, inner = t.stride()
+    if inner != 1 and cols > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    ld = int(t.stride(0)) if rows > 1 else int(cols)
-    return int(t.data_ptr()), (MUSE_F32 if t.dtype == torch.float32 else MUSE_BF16), ld
+    return t.data_ptr(), dtype, step if rows > 1 else cols
 
 
 def _int8_operand(codes, scales, name: str):
@@ -455,45 +456,57 @@ class Int8Linear:
         with _one_device(codes, scales):
             self.workspace = torch.empty(max(int(n.value), 1), dtype=torch.uint8, device=codes.device)
             self.status = torch.zeros(2, dtype=torch.int32, device=codes.device)
+        # what every call passes (a product of a few microseconds should not wait for marshalling)
+        self._torch, self._device = torch, codes.device
+        self._weight = ctypes.byref(self.weight)
+        self._ws, self._ws_bytes, self._status = _ptr(self.workspace), self.workspace.numel(), _ptr(self.status)
 
-    def _out(self, T, out, out_dtype, device):
-        import torch
+    def _run(self, T, device, out, out_dtype, stream, call):
+        """call(out pointer, its muse_dtype and row distance, stream handle) on the holder's device."""
+        torch = self._torch
+        if device != self._device or (out is not None and out.device != device):
+            raise ValueError(f"tensors must be on {self._device}")
         if out is None:
             out = torch.empty((T, self.N), dtype=out_dtype, device=device)
         elif tuple(out.shape) != (T, self.N) or (out_dtype is not None and out.dtype != out_dtype):
             raise ValueError(f"out must be [{T}, {self.N}] of the output type")
-        return (out,) + _rows(out, "out")
+        ptr, dtype, ld = _rows(out, "out")
+        if torch.cuda.current_device() == device.index:
+            call(ptr, dtype, ld, _stream_handle(stream))
+        else:
+            with torch.cuda.device(device):
+                call(ptr, dtype, ld, _stream_handle(stream))
+        return out
 
     def __call__(self, x, out=None, out_dtype=None, stream=None):
         """out[T, out] = x[T, in] W^T, x quantised per row; out in x's type unless given."""
         ptr, dtype, ld = _rows(x, "x")
-        T = int(x.shape[0])
+        T = x.shape[0]
         if x.shape[1] != self.K:
             raise ValueError(f"x has {x.shape[1]} columns, the weights {self.K}")
         if T > self.T_max:
             raise ValueError(f"T={T} exceeds T_max={self.T_max}")
-        out, optr, odtype, ldo = self._out(T, out, out_dtype or (x.dtype if out is None else None), x.device)
-        with _one_device(x, out, self.codes):
-            _check(lib().muse_int8_linear(ptr, dtype, T, self.K, ld, ctypes.byref(self.weight), self.N, optr, odtype,
-                                          ldo, _ptr(self.workspace), self.workspace.numel(), _ptr(self.status),
-                                          _stream_handle(stream)), "muse_int8_linear")
-        return out
+
+        def call(optr, odtype, ldo, st):
+            _check(lib().muse_int8_linear(ptr, dtype, T, self.K, ld, self._weight, self.N, optr, odtype, ldo, self._ws,
+                                          self._ws_bytes, self._status, st), "muse_int8_linear")
+        return self._run(T, x.device, out, out_dtype or (x.dtype if out is None else None), stream, call)
 
     def matmul(self, x_codes, x_scales, out=None, out_dtype=None, stream=None):
         """The product of rows that are quantised already (bfloat16 unless out or out_dtype says
         otherwise); any number of rows."""
-        import torch
         _int8_operand(x_codes, x_scales, "x")
-        T = int(x_codes.shape[0])
+        T = x_codes.shape[0]
         if x_codes.shape[1] != self.K:
             raise ValueError(f"x has {x_codes.shape[1]} columns, the weights {self.K}")
-        out, optr, odtype, ldo = self._out(T, out, out_dtype or (torch.bfloat16 if out is None else None),
-                                           x_codes.device)
-        with _one_device(x_codes, x_scales, out, self.codes):
-            _check(lib().muse_int8_matmul(_ptr(x_codes), _ptr(x_scales), T, self.K, ctypes.byref(self.weight), self.N,
-                                          optr, odtype, ldo, _ptr(self.status), _stream_handle(stream)),
-                   "muse_int8_matmul")
-        return out
+        if x_scales.device != x_codes.device:
+            raise ValueError("x's codes and scales must be on one device")
+
+        def call(optr, odtype, ldo, st):
+            _check(lib().muse_int8_matmul(_ptr(x_codes), _ptr(x_scales), T, self.K, self._weight, self.N, optr, odtype,
+                                          ldo, self._status, st), "muse_int8_matmul")
+        return self._run(T, x_codes.device, out, out_dtype or (self._torch.bfloat16 if out is None else None), stream,
+                         call)
 
     def device_status(self):
         """(status, detail) that bounded waits of this holder's calls recorded; synchronises."""
