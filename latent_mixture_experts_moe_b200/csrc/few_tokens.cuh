@@ -13,7 +13,11 @@
 //   5  out = W_unpool c
 //   6  post norm and residual gate                        (only with those)
 // y and the sublayer's f stay FP32; z, h and c are stored in the type the next product
-// reads (bf16; f16 for NVFP4 experts, whose decoded weights are f16; float32).
+// reads (bf16; f16 for NVFP4 experts, whose decoded weights are f16; float32). bf16 products of
+// intermediates carry up to four tokens as two bf16 numbers each, the rounded value and what
+// rounding took off (16 significant bits), in the MMA's eight columns, which would otherwise be
+// empty: the output's error is then its own rounding (1.7e-3 of its norm instead of 3.7e-3; released
+// norms 4.5e-3). With more than four tokens on an expert (or, unpooler, in the call) one number.
 //
 // Work split: the weight rows of a phase (of all distinct experts in a row) are divided evenly
 // over the CTAs by row, whatever the tile, so no SM waits for another's larger share; a row is
@@ -104,7 +108,7 @@ struct FewGeo {
   }
   // where byte a of an activation row lies
   __device__ static constexpr uint32_t xbyte(uint32_t a) { return FORMAT == FEW_NVFP4 ? a + a / 128 * 16 : a; }
-  // bytes of a stage that holds up to T tokens
+  // bytes of a stage that holds up to T activation rows
   static constexpr uint32_t bytes(int T, bool whole) {
     uint32_t x = 0;
     for (int n = 1; n <= T && !(FORMAT == FEW_NVFP4 && whole); ++n)
@@ -118,6 +122,15 @@ constexpr uint32_t kFewXBytes = 74 * 1024;  // most that an expert's activation 
 // logits of the full-size layer were ready after 8.5 us, with DRAM idle, against 3).
 constexpr int kFewNarrow = 4;
 
+
+// whether n tokens' activations are staged as two bf16 numbers each
+__host__ __device__ constexpr bool few_split(int format, int phase, int n) {
+  return (format == FEW_BF16 || format == FEW_BF16_SHORT) && phase >= 2 && n <= 4;
+}
+// most activation rows of a stage in a call of T tokens
+__host__ __device__ constexpr int few_columns(int format, int T) {
+  return few_split(format, 2, T) ? 2 * T : few_split(format, 2, 4) && T < 8 ? 8 : T;
+}
 
 struct FewArgs {
   int stages;             // ring depth
@@ -275,6 +288,7 @@ struct FewRoute {
   float weight[kFewAssign];
   int pos[kFewAssign];                   // pair -> position
   int token[kFewAssign];                 // position -> token
+  int distinct_of[kFewAssign];           // pair -> number of its expert among the distinct ones
   int ids[kFewAssign];                   // distinct expert -> expert
   int first[kFewAssign + 1];
   uint32_t seen[32];                     // bit e % 32 of word e / 32: expert e is selected
@@ -343,6 +357,7 @@ __device__ __forceinline__ void few_lists(const FewArgs& p, FewRoute& r, int tid
     if (a < A) {
       r.pos[a] = less + same;
       r.token[less + same] = a / p.k;
+      r.distinct_of[a] = d;
       if (same == 0) {
         r.ids[d] = e;
         r.first[d] = less;
@@ -494,7 +509,10 @@ struct FewSource {
   __device__ __forceinline__ const uint8_t* activation(const FewChunks& c, int j) const {
     const void* x = job.phase <= FEW_POOL ? static_cast<const void*>(xin) : gate_up() ? p.z
                   : job.phase == FEW_DOWN ? p.h : p.c;
-    const int row = gate_up() ? r.token[r.first[c.d] + j] : job.phase == FEW_DOWN ? r.first[c.d] + j : j;
+    // (split activations: the second numbers of all rows follow the first ones')
+    const int n = tokens(c), i = j < n ? j : j - n;
+    int row = gate_up() ? r.token[r.first[c.d] + i] : job.phase == FEW_DOWN ? r.first[c.d] + i : i;
+    if (j >= n) row += job.phase == FEW_DOWN ? p.T * p.k : p.T;
     return static_cast<const uint8_t*>(x) + row * (job.K * static_cast<int64_t>(sizeof(TA)));
   }
 };
@@ -531,11 +549,12 @@ __device__ __forceinline__ void few_produce(const FewSource<TA, FORMAT>& q, FewR
     const int n = q.tokens(c), kc = narrow > 0 ? G::kc * narrow : G::depth(n, whole);
     if (pw == 0) {
       const uint32_t xstride = G::xstride(whole ? K : kc), xoff = narrow > 0 ? kFewNarrow * xstride : G::xoff;
-      const uint8_t* x = q.activation(c, min(lane, n - 1));  // lane j: token j's row
+      const int m = few_split(FORMAT, q.job.phase, n) ? 2 * n : n;  // activation rows
+      const uint8_t* x = q.activation(c, min(lane, m - 1));         // lane j: row j
       // `bytes` of every row to dst
       auto rows = [&](uint32_t dst, int bytes) {
 #pragma unroll 1
-        for (int j = 0; j < n; ++j) {
+        for (int j = 0; j < m; ++j) {
           const uint8_t* xj = reinterpret_cast<const uint8_t*>(
               __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x), j));
 #pragma unroll 2
@@ -692,7 +711,7 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, con
   const int g = lane >> 2, t = lane & 3;
   // token rows past n are not staged, and their columns not used; reading none for them saves up
   // to three quarters of the activations' shared-memory cycles (NVFP4, eight tokens: 440 -> 425 us)
-  const bool has_x = g < n;
+  const bool has_x = g < (few_split(FORMAT, phase, n) ? 2 * n : n);
   float acc[8];          // float32: this lane's row, 8 tokens
   float chain[2][2][4];  // MMA: two 16-row tiles, each in two sums, so that fewer MMAs wait for one another
 #pragma unroll
@@ -806,6 +825,23 @@ __device__ __forceinline__ float few_sum(const float* red, int token, int row) {
   return (v[0] + v[1]) + (v[2] + v[3]);
 }
 
+// An intermediate as the next product reads it: bf16 with what its rounding took off, `second`
+// elements further.
+template <typename T>
+__device__ __forceinline__ void few_put(T* a, int64_t second, int64_t i, float v) {
+  const T first = from_f32<T>(v);
+  a[i] = first;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    const float rest = v - to_f32(first);
+    a[second + i] = from_f32<T>(rest == rest ? rest : 0.0f);  // (an infinity stays one)
+  }
+}
+template <typename T>
+__device__ __forceinline__ float few_get(const T* a, int64_t second, int64_t i) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) return to_f32(a[i]) + to_f32(a[second + i]);
+  return to_f32(a[i]);
+}
+
 __device__ __forceinline__ float few_silu(float a) { return a / (1.0f + expf(-a)); }
 
 // Sum over the product warps' threads, the same on each (part: 32 floats).
@@ -817,17 +853,26 @@ __device__ __forceinline__ float few_block_sum(float v, float* part, int wc, int
   return warp_sum(lane < kFewWarps ? part[lane] : 0.0f);
 }
 
-// Centred RMSNorm of one row by the product warps: dst = src / sqrt(mean(src^2) + eps) * (1 + w).
-template <typename TS, typename TG, typename TD>
-__device__ __forceinline__ void few_norm_row(const TS* src, const TG* w, TD* dst, int n, float eps, float* part,
-                                             int tid) {
-  float s = 0.0f;
-  for (int i = tid; i < n; i += 32 * kFewWarps) {
-    const float v = to_f32(src[i]);
+// Centred RMSNorm of n values by the product warps: put(i, get(i) / sqrt(mean(get^2) + eps) * (1 + w_i)).
+template <typename TG, typename Get, typename Put>
+__device__ __forceinline__ void few_norm_row(const TG* w, int n, float eps, float* part, int tid, Get get, Put put) {
+  constexpr int kStep = 32 * kFewWarps, kKeep = 4;  // a thread's first values stay in registers
+  float s = 0.0f, keep[kKeep];
+#pragma unroll
+  for (int j = 0; j < kKeep; ++j) keep[j] = tid + j * kStep < n ? get(tid + j * kStep) : 0.0f;
+#pragma unroll
+  for (int j = 0; j < kKeep; ++j) s = fmaf(keep[j], keep[j], s);
+#pragma unroll 4
+  for (int i = tid + kKeep * kStep; i < n; i += kStep) {
+    const float v = get(i);
     s = fmaf(v, v, s);
   }
   const float scale = 1.0f / sqrtf(few_block_sum(s, part, tid >> 5, tid & 31) / static_cast<float>(n) + eps);
-  for (int i = tid; i < n; i += 32 * kFewWarps) dst[i] = from_f32<TD>(to_f32(src[i]) * scale * (1.0f + to_f32(w[i])));
+#pragma unroll
+  for (int j = 0; j < kKeep; ++j)
+    if (tid + j * kStep < n) put(tid + j * kStep, keep[j] * scale * (1.0f + to_f32(w[tid + j * kStep])));
+#pragma unroll 4
+  for (int i = tid + kKeep * kStep; i < n; i += kStep) put(i, get(i) * scale * (1.0f + to_f32(w[i])));
 }
 
 // c = sum_j g_j y_j / rms_j (1 + gamma) by the product warps, each CTA a slice of it. (All of it in
@@ -835,21 +880,31 @@ __device__ __forceinline__ void few_norm_row(const TS* src, const TG* w, TD* dst
 template <typename TA>
 __device__ __forceinline__ void few_combine(const FewArgs& p, const FewRoute& route, float* scale_s, int wc, int lane,
                                             int tid) {
-  const int T = p.T, L = p.L, k = p.k, nd = route.distinct, rows = nd * L;
+  const int T = p.T, L = p.L, k = p.k, rows = route.distinct * L;
   const TA* gamma = static_cast<const TA*>(p.gamma);
-  // every pair's weight over its root mean square, from the CTAs that hold its rows
-  for (int a = wc; a < T * k; a += kFewWarps) {
-    const int pos = route.pos[a], e = route.expert[a];
-    int d = 0;
-    for (int i = lane; i < nd; i += 32)
-      if (route.ids[i] == e) d = i;
-    d = __reduce_max_sync(0xffffffffu, d);
-    const int c0 = few_owner(rows, d * L), c1 = few_owner(rows, (d + 1) * L - 1);
-    float s = 0.0f;
-    for (int i = c0 + lane; i <= c1; i += 32)  // (with fewer rows than CTAs, some have none)
-      if (few_share(rows, i) < few_share(rows, i + 1)) s += __ldcg(p.ss + static_cast<int64_t>(pos) * kFewGridMax + i);
-    s = warp_sum(s);
-    if (lane == 0) scale_s[a] = route.weight[a] / sqrtf(s / static_cast<float>(L) + p.eps);
+  // every pair's weight over its root mean square, from the CTAs that hold its rows; a warp takes
+  // four pairs at a time, all their loads in flight together
+  for (int a0 = wc; a0 < T * k; a0 += 4 * kFewWarps) {
+    float s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int a = a0 + j * kFewWarps;
+      s[j] = 0.0f;
+      if (a < T * k) {
+        const int pos = route.pos[a], d = route.distinct_of[a];
+        const int c0 = few_owner(rows, d * L), c1 = few_owner(rows, (d + 1) * L - 1);
+#pragma unroll 1
+        for (int i = c0 + lane; i <= c1; i += 32)  // (with fewer rows than CTAs, some have none)
+          if (rows >= static_cast<int>(gridDim.x) || few_share(rows, i) < few_share(rows, i + 1))
+            s[j] += __ldcg(p.ss + static_cast<int64_t>(pos) * kFewGridMax + i);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int a = a0 + j * kFewWarps;
+      const float sum = warp_sum(s[j]);
+      if (lane == 0 && a < T * k) scale_s[a] = route.weight[a] / sqrtf(sum / static_cast<float>(L) + p.eps);
+    }
   }
   few_sync_products();
   for (int i = blockIdx.x * (32 * kFewWarps) + tid; i < T * L; i += gridDim.x * (32 * kFewWarps)) {
@@ -861,7 +916,7 @@ __device__ __forceinline__ void few_combine(const FewArgs& p, const FewRoute& ro
       const float gm = to_f32(gamma[(p.gamma_shared ? 0 : static_cast<int64_t>(route.expert[a]) * L) + f]);
       acc = fmaf(scale_s[a] * (1.0f + gm), __ldcg(p.y + static_cast<int64_t>(route.pos[a]) * L + f), acc);
     }
-    static_cast<TA*>(p.c)[i] = from_f32<TA>(acc);
+    few_put(static_cast<TA*>(p.c), static_cast<int64_t>(T) * L, i, acc);
   }
 }
 
@@ -936,11 +991,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_cons
       if (tid == 0) red_release_u32(counter(i), 1u);  // (cumulative: orders the warps' writes too)
     };
     // the sums of a chunk: store(chunk, token, lane's row, sum) on warp token % kFewStore
-    auto chunk = [&](const FewChunks& c, int n, auto store) {
+    auto chunk = [&](const FewChunks& c, int ph, int n, auto store) {
+      const bool experts = ph == FEW_GATE_UP || ph == FEW_DOWN;
+      const bool split = few_split(experts ? EXPERT : DENSE, ph, n);
       few_mbar_wait(red.full(), red.phase, abort, p.status, 0xE00u);
       __syncwarp();
 #pragma unroll 1
-      for (int j = ws; j < n; j += kFewStore) store(c, j, few_sum(red.red(), j, lane));
+      for (int j = ws; j < n; j += kFewStore) {
+        float v = few_sum(red.red(), j, lane);
+        if (split) v += few_sum(red.red(), n + j, lane);
+        store(c, j, v);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(red.free());
       red.next();
@@ -949,7 +1010,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_cons
       const FewJob job = few_job(p, ph, route.distinct);
 #pragma unroll 1
       for (FewChunks c(job.U, job.group, job.most); !c.done(); c.next())
-        chunk(c, ph == FEW_GATE_UP || ph == FEW_DOWN ? route.first[c.d + 1] - route.first[c.d] : T, store);
+        chunk(c, ph, ph == FEW_GATE_UP || ph == FEW_DOWN ? route.first[c.d + 1] - route.first[c.d] : T, store);
     };
     each(FEW_ROUTER, [&](const FewChunks& c, int j, float v) {
       if (lane < c.len) p.logits[static_cast<int64_t>(j) * E + c.f + lane] = v;
@@ -970,8 +1031,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_cons
           for (int t = ws; t < T; t += kFewStore) few_route(p, route, t, lane);
           routed = true;
         } else if (routed || __all_sync(0xffffffffu, *abort != 0 || mbar_try_wait(red.full(), red.phase))) {
-          chunk(c, T, [&](const FewChunks& cc, int j, float v) {
-            if (lane < cc.len) static_cast<TZ*>(p.z)[static_cast<int64_t>(j) * L + cc.f + lane] = from_f32<TZ>(v);
+          chunk(c, FEW_POOL, T, [&](const FewChunks& cc, int j, float v) {
+            if (lane < cc.len)
+              few_put(static_cast<TZ*>(p.z), static_cast<int64_t>(T) * L, static_cast<int64_t>(j) * L + cc.f + lane, v);
           });
           c.next();
         }
@@ -988,8 +1050,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_cons
         mu = p.m_up[route.ids[c.d]];
       }
       if (lane < c.len)
-        static_cast<TZ*>(p.h)[static_cast<int64_t>(route.first[c.d] + j) * I + c.f + lane] =
-            from_f32<TZ>(few_silu(v * mg) * (u * mu));
+        few_put(static_cast<TZ*>(p.h), static_cast<int64_t>(T) * p.k * I,
+                static_cast<int64_t>(route.first[c.d] + j) * I + c.f + lane, few_silu(v * mg) * (u * mu));
     });
     arrive(FEW_H);
     {
@@ -1063,8 +1125,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_cons
   };
   if (pre) {
     for (int t = blockIdx.x; t < T; t += gridDim.x)
-      few_norm_row(static_cast<const TA*>(p.x) + static_cast<int64_t>(t) * D, static_cast<const TA*>(p.ffn_pre_gain),
-                   static_cast<TA*>(p.xn) + static_cast<int64_t>(t) * D, D, p.ffn_pre_eps, part, tid);
+      few_norm_row(
+          static_cast<const TA*>(p.ffn_pre_gain), D, p.ffn_pre_eps, part, tid,
+          [&](int i) { return to_f32(static_cast<const TA*>(p.x)[static_cast<int64_t>(t) * D + i]); },
+          [&](int i, float v) { static_cast<TA*>(p.xn)[static_cast<int64_t>(t) * D + i] = from_f32<TA>(v); });
     arrive(FEW_XN);
   }
 #pragma unroll 1
@@ -1074,8 +1138,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_cons
         wait(FEW_Z);
         TZ* z = static_cast<TZ*>(p.z);
         for (int t = blockIdx.x; t < T; t += gridDim.x)
-          few_norm_row(z + static_cast<int64_t>(t) * L, static_cast<const TA*>(p.pre_norm_gain),
-                       z + static_cast<int64_t>(t) * L, L, p.pre_norm_eps, part, tid);
+          few_norm_row(
+              static_cast<const TA*>(p.pre_norm_gain), L, p.pre_norm_eps, part, tid,
+              [&](int i) { return few_get(z, static_cast<int64_t>(T) * L, static_cast<int64_t>(t) * L + i); },
+              [&](int i, float v) { few_put(z, static_cast<int64_t>(T) * L, static_cast<int64_t>(t) * L + i, v); });
         arrive(FEW_ZN);
       }
       few_sync_all();

@@ -1445,11 +1445,12 @@ FewLayout few_layout(const muse_moe_config& c) {
   };
   l.logits = take(sizeof(float) * T * c.E);
   l.xn = take(c.ffn_pre_gain != nullptr ? as * T * c.D : 0);
-  l.z = take(as * T * c.L);
-  l.h = take(as * A * c.I);
+  // (4 bytes each: float32, or two bf16 numbers)
+  l.z = take(4 * T * c.L);
+  l.h = take(4 * A * c.I);
   l.y = take(sizeof(float) * A * c.L);
   l.ss = take(sizeof(float) * A * kFewGridMax);
-  l.c = take(as * T * c.L);
+  l.c = take(4 * T * c.L);
   l.f = take(finish ? sizeof(float) * T * c.D : 0);
   l.ssf = take(finish ? sizeof(float) * T * kFewGridMax : 0);
   l.total = o;
@@ -1466,7 +1467,8 @@ muse_status launch_few(FewArgs& a, cudaStream_t st) {
   const uint32_t x = FP4 ? a.T * FewGeo<FEW_NVFP4>::xstride(std::max(a.L, a.I)) : 0;
   a.x_bytes = x <= kFewXBytes ? static_cast<uint32_t>(align_up(x, 128)) : 0;
   a.stage_bytes = static_cast<uint32_t>(
-      align_up(std::max(FewGeo<kDense>::bytes(a.T, false), FewGeo<kExpert>::bytes(a.T, a.x_bytes > 0)), 128));
+      align_up(std::max(FewGeo<kDense>::bytes(few_columns(kDense, a.T), false),
+                        FewGeo<kExpert>::bytes(few_columns(kExpert, a.T), a.x_bytes > 0)), 128));
   a.narrow = 0;
   if (cdiv(a.E, grid) <= kFewNarrow)
     for (int f = 2; f <= 4 && (kFewNarrow + a.T) * FewGeo<kDense>::xstride(f * FewGeo<kDense>::kc) <= a.stage_bytes; f *= 2)
