@@ -62,7 +62,7 @@ __device__ __forceinline__ uint2 int8_codes8(const float (&v)[8], float scale, f
 // eight consecutive values; ALIGNED: from a 16-byte boundary
 template <typename T, bool ALIGNED>
 struct Int8Load {
-  T raw[8];
+  alignas(16) T raw[8];
   __device__ __forceinline__ void load(const T* p) {
     if constexpr (ALIGNED) {
 #pragma unroll
@@ -71,6 +71,19 @@ struct Int8Load {
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) raw[i] = p[i];
+    }
+  }
+  // the largest magnitude's bits (see magnitude_bits), and a: bf16 two at a time
+  __device__ __forceinline__ uint32_t amax(uint32_t a) const {
+    if constexpr (sizeof(T) == 2) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = __vmaxu2(m, reinterpret_cast<const uint32_t*>(raw)[i] & 0x7fff7fffu);
+      return max(a, max(m << 16, m & 0xffff0000u));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a = max(a, magnitude_bits(to_f32(raw[i])));
+      return a;
     }
   }
   __device__ __forceinline__ void get(float (&v)[8]) const {
@@ -103,20 +116,12 @@ __global__ void __launch_bounds__(256, 5) k_quant_rows_int8(const T* __restrict_
   }
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    if ((i * TPR + sub) * 8 < K) {
-      float v[8];
-      hold[i].get(v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = max(amax, magnitude_bits(v[j]));
-    }
+    if ((i * TPR + sub) * 8 < K) amax = hold[i].amax(amax);
   }
   for (int k = (kVecs * TPR + sub) * 8; k < K; k += TPR * 8) {
     Int8Load<T, ALIGNED> more;
     more.load(x + k);
-    float v[8];
-    more.get(v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) amax = max(amax, magnitude_bits(v[j]));
+    amax = more.amax(amax);
   }
   amax = __reduce_max_sync(0xffffffffu, amax);
   if constexpr (TPR > 32) {
@@ -280,12 +285,7 @@ __global__ void __launch_bounds__(Int8Stream<NT, FUSED>::kThreads, 1) k_int8_str
     uint32_t amax = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if ((i * 32 * per + sub) * 8 < K) {
-        float v[8];
-        hold[i].get(v);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) amax = max(amax, magnitude_bits(v[q]));
-      }
+      if ((i * 32 * per + sub) * 8 < K) amax = hold[i].amax(amax);
     }
     amax = __reduce_max_sync(0xffffffffu, amax);
     if (lane == 0) part[wc] = amax;
