@@ -361,7 +361,7 @@ typedef struct muse_int8_weight {
 
 /* rows x K values of type dtype (muse_dtype; aligned to their type, row r at src + r * ld) ->
  * codes int8 [rows, K] (16-byte aligned) and scales float [rows]. K a multiple of 16, at
- * most 2^20; ld >= K. Enqueued on `stream`. */
+ * most 2^20; ld >= K. codes and scales may not overlap src. Enqueued on `stream`. */
 MUSE_API muse_status muse_quantize_int8_rows(const void* src, int32_t dtype, int64_t rows, int64_t K, int64_t ld,
                                              void* codes, float* scales, void* stream);
 
@@ -388,9 +388,11 @@ MUSE_API muse_status muse_int8_linear(const void* x, int32_t x_dtype, int64_t T,
  * of muse_latent_moe_forward with the same arguments and options, for interactive decoding,
  * where the launches of the forward cost more than their work. It differs in rounding only:
  * expert outputs and the sublayer's f stay FP32, float32 workloads multiply in FP32 (not
- * TF32), and with NVFP4 experts the latent is rounded to f16 once. It requires 16-bit or
- * float32 activations (MUSE_ACT_NVFP4 is UNSUPPORTED); NVFP4 experts require L and I
- * multiples of 256; int8 projections are UNSUPPORTED. stage_events is ignored. cfg->workspace: device, 256-byte aligned,
+ * TF32), NVFP4 experts read the latent rounded to f16 once, and where at most 4 tokens meet a
+ * bf16 weight, the latent, hidden rows and combined latent carry 16 bits of mantissa (two
+ * bf16 numbers each). It requires 16-bit or float32 activations (MUSE_ACT_NVFP4 is
+ * UNSUPPORTED); NVFP4 experts require L and I multiples of 256; int8 projections are
+ * UNSUPPORTED. stage_events is ignored. cfg->workspace: device, 256-byte aligned,
  * muse_latent_moe_few_tokens_workspace_size bytes, a layout of its own; calls whose work
  * overlaps on the GPU need workspaces of their own. The kernel is launched cooperatively
  * (its CTAs, one per SM, wait for one another): MUSE_ERR_CUDA where the device cannot hold

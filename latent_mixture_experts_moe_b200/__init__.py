@@ -651,9 +651,11 @@ class LatentMoE:
         if T > min(self.T_max, FEW_TOKENS):
             raise ValueError(f"T={T} exceeds {min(self.T_max, FEW_TOKENS)}")
         for t, dtype in ((topk_idx, torch.int32), (topk_w, torch.float32)):
-            if t is not None and (t.shape != (T, self.dims["k"]) or t.dtype != dtype or t.device != x.device):
-                raise ValueError(f"topk_idx and topk_w are [{T}, {self.dims['k']}] int32 and float32 on x's device")
-        with _one_device(x, self.w["W_router"]):
+            if t is not None and (t.shape != (T, self.dims["k"]) or t.dtype != dtype or t.device != x.device
+                                  or not t.is_contiguous()):
+                raise ValueError(f"topk_idx and topk_w are contiguous [{T}, {self.dims['k']}] int32 and float32 tensors "
+                                 "on x's device")
+        with _one_device(x, self.w["W_router"], x if out is None else out):
             cfg = Config.from_buffer_copy(self._few_config)
             cfg.T, cfg.topk_idx_out, cfg.topk_w_out = T, _ptr(topk_idx), _ptr(topk_w)
             if out is None:

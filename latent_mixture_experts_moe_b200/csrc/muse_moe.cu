@@ -1551,6 +1551,26 @@ muse_status few_tokens_impl(const muse_moe_config& c, const void* x, const void*
   return c.dtype == MUSE_BF16 ? launch_few<__nv_bfloat16, false>(a, st) : launch_few<float, false>(a, st);
 }
 
+// Whether two blocks of rows (bytes per row, distance between rows) share a byte. Blocks whose rows
+// lie equally far apart may be column ranges of one buffer.
+bool rows_overlap(const void* a, int64_t rows_a, int64_t bytes_a, int64_t step_a, const void* b, int64_t rows_b,
+                  int64_t bytes_b, int64_t step_b) {
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+  if (pa + (rows_a - 1) * step_a + bytes_a <= pb || pb + (rows_b - 1) * step_b + bytes_b <= pa) return false;
+  if (step_a != step_b || rows_a == 1 || rows_b == 1) return true;
+  const int64_t column = ((static_cast<int64_t>(pb - pa) % step_a) + step_a) % step_a;
+  return column < bytes_a || column + bytes_b > step_a;
+}
+
+// out [T, N] of an int8 product against its rows x and weights
+bool int8_out_overlaps(const void* out, int64_t T, int64_t N, int32_t out_dtype, int64_t ldo, const void* x,
+                       int64_t x_size, int64_t K, int64_t ldx, const muse_int8_weight& w) {
+  const int64_t size = static_cast<int64_t>(dtype_size(out_dtype));
+  return rows_overlap(out, T, N * size, ldo * size, x, T, K * x_size, ldx * x_size) ||
+         rows_overlap(out, T, N * size, ldo * size, w.codes, 1, N * K, N * K) ||
+         rows_overlap(out, T, N * size, ldo * size, w.scales, 1, 4 * N, 4 * N);
+}
+
 // the sizes, weights and output of an int8 product
 muse_status validate_int8(int64_t T, int64_t K, const muse_int8_weight* w, int64_t N, const void* out,
                           int32_t out_dtype, int64_t ldo, const uint32_t* status) {
@@ -1861,6 +1881,10 @@ muse_status muse_quantize_int8_rows(const void* src, int32_t dtype, int64_t rows
   if (rows == 0) return MUSE_OK;
   if (!aligned_to(src, dtype_size(dtype)) || !aligned_to(codes, 16) || !aligned_to(scales, 4))
     return MUSE_ERR_INVALID_ARG;
+  const int64_t size = static_cast<int64_t>(dtype_size(dtype));
+  if (rows_overlap(src, rows, K * size, ld * size, codes, 1, rows * K, rows * K) ||
+      rows_overlap(src, rows, K * size, ld * size, scales, 1, 4 * rows, 4 * rows))
+    return MUSE_ERR_INVALID_ARG;
   return quantize_int8(src, dtype, rows, K, ld, codes, scales, static_cast<cudaStream_t>(stream));
 }
 
@@ -1870,6 +1894,10 @@ muse_status muse_int8_matmul(const void* x_codes, const float* x_scales, int64_t
   MUSE_TRY(validate_int8(T, K, w, N, out, out_dtype, ldo, status));
   if (T == 0) return MUSE_OK;
   if (!aligned_to(x_codes, 16) || !aligned_to(x_scales, 4)) return MUSE_ERR_INVALID_ARG;
+  if (int8_out_overlaps(out, T, N, out_dtype, ldo, x_codes, 1, K, K, *w) ||
+      rows_overlap(out, T, N * static_cast<int64_t>(dtype_size(out_dtype)), ldo * static_cast<int64_t>(dtype_size(out_dtype)),
+                   x_scales, 1, 4 * T, 4 * T))
+    return MUSE_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return int8_product(x_codes, x_scales, T, K, *w, N, out, out_dtype, ldo, status, false, st);
 }
@@ -1888,7 +1916,9 @@ muse_status muse_int8_linear(const void* x, int32_t x_dtype, int64_t T, int64_t 
   if (!valid_dtype(x_dtype) || ldx < K) return MUSE_ERR_INVALID_ARG;
   if (ldx > (int64_t(1) << 40)) return MUSE_ERR_UNSUPPORTED;
   if (T == 0) return MUSE_OK;
-  if (!aligned_to(x, dtype_size(x_dtype))) return MUSE_ERR_INVALID_ARG;
+  if (!aligned_to(x, dtype_size(x_dtype)) ||
+      int8_out_overlaps(out, T, N, out_dtype, ldo, x, static_cast<int64_t>(dtype_size(x_dtype)), K, ldx, *w))
+    return MUSE_ERR_INVALID_ARG;
   size_t need = 0;
   MUSE_TRY(muse_int8_linear_workspace_size(T, K, &need));
   if (!aligned_to(workspace, kAlign) || workspace_bytes < need) return MUSE_ERR_WORKSPACE;

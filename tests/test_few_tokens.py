@@ -343,3 +343,19 @@ def test_checked_form_refuses_shapes_and_overlap():
     args = _checked_args(cfg)
     args["out"].data = args["x"].data
     assert call(args) == 1
+
+
+@pytest.mark.gpu
+def test_holder_refuses_routing_outputs_it_cannot_write():
+    """Wrong shape, type or layout (the kernel writes [T, k] values one after the other)."""
+    w = workload("routing_outputs", 4, 256, 128, 128, 8, 2)
+    inp = make_inputs(w)
+    layer = moe.LatentMoE({n: t for n, t in inp.items() if n != "x"}, T_max=4, k=w.k, eps=w.eps)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    for idx in (torch.zeros(4, 3, **i32), torch.zeros(4, 2, dtype=torch.int64, device="cuda"),
+                torch.zeros(2, 4, **i32).t(), torch.zeros(1, 2, **i32).expand(4, 2),
+                torch.zeros(4, 2, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            layer.few_tokens(inp["x"], topk_idx=idx)
+    with pytest.raises(ValueError):
+        layer.few_tokens(inp["x"], topk_w=torch.zeros(1, 1, device="cuda").expand(4, 2))

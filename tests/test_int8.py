@@ -228,6 +228,34 @@ def test_quantiser_refuses_bad_arguments_before_any_launch():
     assert call(rows=0) == 0
 
 
+def test_outputs_over_inputs_are_refused():
+    base, far = 1 << 22, 1 << 26
+
+    def quantise(codes, scales, ld=64):  # float32 [3, 64]
+        return moe.lib().muse_quantize_int8_rows(base, 0, 3, 64, ld, codes, scales, None)
+    for at in (base, base + 2 * 4 * 64 + 3 * 64):
+        assert quantise(at, far) == 1
+    assert quantise(base - 3 * 64 + 16, far) == 1
+    assert quantise(far, base + 764) == 1
+    size = dict(K=64, N=32)
+    # x codes [4, 64] at base; out float32 [4, 32]
+    for out in (base, base + 252, base - 4 * 4 * 32 + 4):
+        assert _matmul(x=base, out=out, **size) == 1
+    assert _matmul(out=(1 << 20) + 2044, **size) == 1             # over the weights' codes
+    assert _matmul(out=(1 << 21) + 124, **size) == 1              # over their scales
+    assert _matmul(out=(1 << 23) + 12, **size) == 1               # over x's scales
+    w, n = _weight(), ctypes.c_size_t(0)
+    moe.lib().muse_int8_linear_workspace_size(4, 64, ctypes.byref(n))
+
+    def linear(out, ldx, ldo, nb=n.value):  # bf16 in and out; nb one short: accepted arguments give 3
+        return moe.lib().muse_int8_linear(base, 1, 4, 64, ldx, ctypes.byref(w), 32, out, 1, ldo, far, nb, None, None)
+    assert linear(base, 64, 32) == 1 and linear(base + 2 * 64, 128, 64) == 1
+    # column ranges of one buffer of 128 columns: after the inputs, one too early, wrapped into the next row
+    assert linear(base + 2 * 64, 128, 128, 0) == 3 and linear(base + 2 * 96, 128, 128, 0) == 3
+    assert linear(base + 2 * 63, 128, 128) == 1 and linear(base + 2 * 97, 128, 128) == 1
+    assert linear(base - 2 * 32, 128, 128, 0) == 3 and linear(base - 2 * 31, 128, 128) == 1
+
+
 def test_binding_refuses_wrong_tensors():
     codes, scales = torch.zeros(32, 64, dtype=torch.int8), torch.zeros(32)
     with pytest.raises(ValueError):
