@@ -388,9 +388,9 @@ MUSE_API muse_status muse_int8_linear(const void* x, int32_t x_dtype, int64_t T,
  * of muse_latent_moe_forward with the same arguments and options, for interactive decoding,
  * where the launches of the forward cost more than their work. It differs in rounding only:
  * expert outputs and the sublayer's f stay FP32, float32 workloads multiply in FP32 (not
- * TF32), NVFP4 experts read the latent rounded to f16 once, and where at most 4 tokens meet a
- * bf16 weight, the latent, hidden rows and combined latent carry 16 bits of mantissa (two
- * bf16 numbers each). It requires 16-bit or float32 activations (MUSE_ACT_NVFP4 is
+ * TF32), NVFP4 experts read the latent and the hidden rows rounded to f16 once, and where bf16
+ * weights multiply the latent, hidden rows or combined latent, these carry 16 significant
+ * bits (two bf16 numbers each). It requires 16-bit or float32 activations (MUSE_ACT_NVFP4 is
  * UNSUPPORTED); NVFP4 experts require L and I multiples of 256; int8 projections are
  * UNSUPPORTED. stage_events is ignored. cfg->workspace: device, 256-byte aligned,
  * muse_latent_moe_few_tokens_workspace_size bytes, a layout of its own; calls whose work

@@ -14,25 +14,25 @@
 //   6  post norm and residual gate                        (only with those)
 // y and the sublayer's f stay FP32; z, h and c are stored in the type the next product
 // reads (bf16; f16 for NVFP4 experts, whose decoded weights are f16; float32). bf16 products of
-// intermediates carry up to four tokens as two bf16 numbers each, the rounded value and what
-// rounding took off (16 significant bits), in the MMA's eight columns, which would otherwise be
-// empty: the output's error is then its own rounding (1.7e-3 of its norm instead of 3.7e-3; released
-// norms 4.5e-3). With more than four tokens on an expert (or, unpooler, in the call) one number.
+// intermediates carry a token as two bf16 numbers, the rounded value and what rounding took off
+// (16 significant bits): up to four tokens in the MMA's eight columns, which would otherwise be
+// empty, more in a second MMA. The output's error is then its own rounding (1.7e-3 of its norm
+// instead of 3.7e-3; released norms 4.5e-3).
 //
 // Work split: the weight rows of a phase (of all distinct experts in a row) are divided evenly
 // over the CTAs by row, whatever the tile, so no SM waits for another's larger share; a row is
 // always summed whole, by the same warps in the same order, so its result does not depend on
 // the split.
 //
-// Roles (24 warps). Producers (4): three stream a CTA's weight rows through a ring of stages, up
+// Roles (16 warps). Producers (4): three stream a CTA's weight rows through a ring of stages, up
 // to 32 rows x kc elements each, by 16-byte asynchronous copies (any row count and row start;
 // the row distance in shared memory is padded so that the fragment reads below are free of
 // bank conflicts); the fourth adds the n <= 8 activation rows of the same K range. At a phase's
 // start the ring fills with the new phase's weights while the grid barrier is still pending
 // -- only the activations wait for it -- so DRAM stays busy through the barriers. (One bulk
 // copy per row piece, from one producer warp, instead: one token through the full-size bf16
-// layer in 331 us, against 171 with these copies.)
-// Products (16): they split each stage along K. 16-bit weights go to the warp-level MMA (m16n8k16:
+// layer in 331 us, against 171 with these copies at the time, 162 now.)
+// Products (8; with 16, NVFP4 120 us against 97): they split each stage along K. 16-bit weights go to the warp-level MMA (m16n8k16:
 // weight rows as A, the tokens as its 8 columns): lane (g, t) of a warp reads 16 consecutive
 // bytes of rows g and g + 8 and of token g, and the MMA's K order is that of these bytes in both
 // operands. NVFP4 rows are decoded in registers into the A fragment (gemv_fp4.cuh). float32 rows
@@ -80,7 +80,7 @@ enum FewFormat : int { FEW_BF16 = 0, FEW_NVFP4 = 1, FEW_F32 = 2, FEW_BF16_SHORT 
 // 2048 elements of NVFP4 rows are as many bytes as 512 of bf16, but each activation row would
 // take 4 KB of every stage, most of a stage's time with several tokens on an expert: where they
 // fit (FewArgs::x_bytes), an expert's activation rows lie whole in a buffer of their own, copied
-// once for all of a CTA's rows of that expert (16 experts with four tokens each: 390 us without);
+// once for all of a CTA's rows of that expert (16 experts with four tokens each: 158 us, 390 without);
 // otherwise its stages hold less of K (depth).
 // FEW_BF16_SHORT: the dense products beside NVFP4 experts, whose ring is shorter by that buffer.
 // The row distances keep the product warps' reads free of bank conflicts: bf16 rows 64 bytes
@@ -123,14 +123,12 @@ constexpr uint32_t kFewXBytes = 74 * 1024;  // most that an expert's activation 
 constexpr int kFewNarrow = 4;
 
 
-// whether n tokens' activations are staged as two bf16 numbers each
-__host__ __device__ constexpr bool few_split(int format, int phase, int n) {
-  return (format == FEW_BF16 || format == FEW_BF16_SHORT) && phase >= 2 && n <= 4;
+// whether a phase's activations are staged as two bf16 numbers each
+__host__ __device__ constexpr bool few_split(int format, int phase) {
+  return (format == FEW_BF16 || format == FEW_BF16_SHORT) && phase >= 2;
 }
 // most activation rows of a stage in a call of T tokens
-__host__ __device__ constexpr int few_columns(int format, int T) {
-  return few_split(format, 2, T) ? 2 * T : few_split(format, 2, 4) && T < 8 ? 8 : T;
-}
+__host__ __device__ constexpr int few_columns(int format, int T) { return few_split(format, 2) ? 2 * T : T; }
 
 struct FewArgs {
   int stages;             // ring depth
@@ -549,7 +547,7 @@ __device__ __forceinline__ void few_produce(const FewSource<TA, FORMAT>& q, FewR
     const int n = q.tokens(c), kc = narrow > 0 ? G::kc * narrow : G::depth(n, whole);
     if (pw == 0) {
       const uint32_t xstride = G::xstride(whole ? K : kc), xoff = narrow > 0 ? kFewNarrow * xstride : G::xoff;
-      const int m = few_split(FORMAT, q.job.phase, n) ? 2 * n : n;  // activation rows
+      const int m = few_split(FORMAT, q.job.phase) ? 2 * n : n;  // activation rows
       const uint8_t* x = q.activation(c, min(lane, m - 1));         // lane j: row j
       // `bytes` of every row to dst
       auto rows = [&](uint32_t dst, int bytes) {
@@ -711,7 +709,10 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, con
   const int g = lane >> 2, t = lane & 3;
   // token rows past n are not staged, and their columns not used; reading none for them saves up
   // to three quarters of the activations' shared-memory cycles (NVFP4, eight tokens: 440 -> 425 us)
-  const bool has_x = g < (few_split(FORMAT, phase, n) ? 2 * n : n);
+  // (two numbers for each token: in columns of their own, or with more than four tokens in a second
+  // MMA that adds to the first one's sums)
+  const bool split = few_split(FORMAT, phase), twice = split && n > 4;
+  const bool has_x = g < (split && !twice ? 2 * n : n);
   float acc[8];          // float32: this lane's row, 8 tokens
   float chain[2][2][4];  // MMA: two 16-row tiles, each in two sums, so that fewer MMAs wait for one another
 #pragma unroll
@@ -745,6 +746,13 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, con
         mma_bf16_16816(chain[0][1], a2.x, a3.x, a2.y, a3.y, b.x, b.y);
         mma_bf16_16816(chain[1][0], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
         mma_bf16_16816(chain[1][1], a2.z, a3.z, a2.w, a3.w, b.z, b.w);
+        if (twice) {
+          const uint4 c = lds128_if(has_x, x + n * xstride + o);
+          mma_bf16_16816(chain[0][0], a0.x, a1.x, a0.y, a1.y, c.x, c.y);
+          mma_bf16_16816(chain[0][1], a2.x, a3.x, a2.y, a3.y, c.x, c.y);
+          mma_bf16_16816(chain[1][0], a0.z, a1.z, a0.w, a1.w, c.z, c.w);
+          mma_bf16_16816(chain[1][1], a2.z, a3.z, a2.w, a3.w, c.z, c.w);
+        }
       }
     } else if constexpr (FORMAT == FEW_NVFP4) {
       const uint32_t w = st + g * G::wstride + t * 16u;
@@ -993,7 +1001,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_cons
     // the sums of a chunk: store(chunk, token, lane's row, sum) on warp token % kFewStore
     auto chunk = [&](const FewChunks& c, int ph, int n, auto store) {
       const bool experts = ph == FEW_GATE_UP || ph == FEW_DOWN;
-      const bool split = few_split(experts ? EXPERT : DENSE, ph, n);
+      const bool split = few_split(experts ? EXPERT : DENSE, ph) && n <= 4;  // (sums in two columns)
       few_mbar_wait(red.full(), red.phase, abort, p.status, 0xE00u);
       __syncwarp();
 #pragma unroll 1
