@@ -549,16 +549,30 @@ __device__ __forceinline__ void few_produce(const FewSource<TA, FORMAT>& q, FewR
       const uint32_t xstride = G::xstride(whole ? K : kc), xoff = narrow > 0 ? kFewNarrow * xstride : G::xoff;
       const int m = few_split(FORMAT, q.job.phase) ? 2 * n : n;  // activation rows
       const uint8_t* x = q.activation(c, min(lane, m - 1));         // lane j: row j
-      // `bytes` of every row to dst
-      auto rows = [&](uint32_t dst, int bytes) {
+      // `bytes` of every row to dst, BATCH rows at a time: row by row this warp did not keep up with
+      // the weights (eight tokens, eight bf16 experts, full size: 215 us, 393 row by row; four
+      // tokens of the released sizes: 43, 49)
+      auto copy = [&](uint32_t dst, int bytes, auto batch) {
+        constexpr int BATCH = decltype(batch)::value;
 #pragma unroll 1
-        for (int j = 0; j < m; ++j) {
-          const uint8_t* xj = reinterpret_cast<const uint8_t*>(
-              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x), j));
-#pragma unroll 2
-          for (int a = 16 * lane; a - 16 * lane < bytes; a += 512)
-            cp_async16_if(a < bytes, dst + xstride * j + G::xbyte(a), xj + a);
+        for (int j = 0; j < m; j += BATCH) {
+          const uint8_t* xj[BATCH];
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i)
+            xj[i] = reinterpret_cast<const uint8_t*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x), j + i));
+#pragma unroll (BATCH == 1 ? 2 : 1)
+          for (int a = 16 * lane; a - 16 * lane < bytes; a += 512) {
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i)
+              cp_async16_if(a < bytes && j + i < m, dst + xstride * (j + i) + G::xbyte(a), xj[i] + a);
+          }
         }
+      };
+      auto rows = [&](uint32_t dst, int bytes) {
+        if (m == 1) copy(dst, bytes, std::integral_constant<int, 1>{});
+        else if (m <= 4) copy(dst, bytes, std::integral_constant<int, 4>{});
+        else copy(dst, bytes, std::integral_constant<int, 8>{});
       };
       if (whole && c.d != expert) {
         expert = c.d;
@@ -708,7 +722,7 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, con
   using G = FewGeo<FORMAT>;
   const int g = lane >> 2, t = lane & 3;
   // token rows past n are not staged, and their columns not used; reading none for them saves up
-  // to three quarters of the activations' shared-memory cycles (NVFP4, eight tokens: 440 -> 425 us)
+  // to three quarters of the activations' shared-memory cycles (NVFP4, eight tokens: 425 us, 440 reading all)
   // (two numbers for each token: in columns of their own, or with more than four tokens in a second
   // MMA that adds to the first one's sums)
   const bool split = few_split(FORMAT, phase), twice = split && n > 4;
@@ -737,23 +751,27 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewRing& ring, con
       const uint32_t w = st + (narrow > 0 ? g & (kFewNarrow - 1) : g) * wstride + t * 16u;
       const uint32_t x = st + xoff + g * xstride + t * 16u;
       const uint32_t r8 = narrow > 0 ? 0u : 8u * wstride;
+      auto products = [&](auto two) {
 #pragma unroll 2
-      for (int s = wc; s < kn / 32; s += kFewWarps) {  // 32 elements = 64 bytes of each row
-        const uint32_t o = 64u * s;
-        const uint4 b = lds128_if(has_x, x + o), a0 = lds128(w + o), a1 = lds128(w + r8 + o), a2 = lds128(w + 2 * r8 + o),
-                    a3 = lds128(w + 3 * r8 + o);
-        mma_bf16_16816(chain[0][0], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
-        mma_bf16_16816(chain[0][1], a2.x, a3.x, a2.y, a3.y, b.x, b.y);
-        mma_bf16_16816(chain[1][0], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
-        mma_bf16_16816(chain[1][1], a2.z, a3.z, a2.w, a3.w, b.z, b.w);
-        if (twice) {
-          const uint4 c = lds128_if(has_x, x + n * xstride + o);
-          mma_bf16_16816(chain[0][0], a0.x, a1.x, a0.y, a1.y, c.x, c.y);
-          mma_bf16_16816(chain[0][1], a2.x, a3.x, a2.y, a3.y, c.x, c.y);
-          mma_bf16_16816(chain[1][0], a0.z, a1.z, a0.w, a1.w, c.z, c.w);
-          mma_bf16_16816(chain[1][1], a2.z, a3.z, a2.w, a3.w, c.z, c.w);
+        for (int s = wc; s < kn / 32; s += kFewWarps) {  // 32 elements = 64 bytes of each row
+          const uint32_t o = 64u * s;
+          const uint4 b = lds128_if(has_x, x + o), a0 = lds128(w + o), a1 = lds128(w + r8 + o), a2 = lds128(w + 2 * r8 + o),
+                      a3 = lds128(w + 3 * r8 + o);
+          mma_bf16_16816(chain[0][0], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
+          mma_bf16_16816(chain[0][1], a2.x, a3.x, a2.y, a3.y, b.x, b.y);
+          mma_bf16_16816(chain[1][0], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+          mma_bf16_16816(chain[1][1], a2.z, a3.z, a2.w, a3.w, b.z, b.w);
+          if constexpr (decltype(two)::value) {
+            const uint4 c = lds128_if(has_x, x + n * xstride + o);
+            mma_bf16_16816(chain[0][0], a0.x, a1.x, a0.y, a1.y, c.x, c.y);
+            mma_bf16_16816(chain[0][1], a2.x, a3.x, a2.y, a3.y, c.x, c.y);
+            mma_bf16_16816(chain[1][0], a0.z, a1.z, a0.w, a1.w, c.z, c.w);
+            mma_bf16_16816(chain[1][1], a2.z, a3.z, a2.w, a3.w, c.z, c.w);
+          }
         }
-      }
+      };
+      if (twice) products(std::true_type{});
+      else products(std::false_type{});
     } else if constexpr (FORMAT == FEW_NVFP4) {
       const uint32_t w = st + g * G::wstride + t * 16u;
       const uint32_t x = (whole ? xbuf.base + k0 / 8 * 18 : st + G::xoff) + g * xstride + t * 64u + (t >> 1) * 16u;
