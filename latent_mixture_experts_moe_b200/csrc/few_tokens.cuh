@@ -40,7 +40,7 @@
 // chunk of rows go to one of two buffers.
 // Store (4): they add the partial sums in a fixed order, apply what follows the product and
 // write the result, while the product warps go on with the next chunk. The router's rows come
-// first, so that two store warps select the experts while the pooler's rows stream.
+// first, so that the store warps select the experts while the pooler's rows stream.
 #pragma once
 
 #include <cstdint>
@@ -859,7 +859,7 @@ __device__ __forceinline__ void few_put(T* a, int64_t second, int64_t i, float v
   a[i] = first;
   if constexpr (std::is_same<T, __nv_bfloat16>::value) {
     const float rest = v - to_f32(first);
-    a[second + i] = from_f32<T>(rest == rest ? rest : 0.0f);  // (an infinity stays one)
+    a[second + i] = from_f32<T>(fabsf(rest) < INFINITY ? rest : 0.0f);  // (infinities and NaN stay what they are)
   }
 }
 template <typename T>
