@@ -104,6 +104,8 @@ SHAPES = [
     ("wide_model", 6, 10368, 128, 128, 3, 2, "bf16"),
     ("many_experts", 8, 256, 128, 128, 1000, 8, "bf16"),
     ("many_per_token", 8, 256, 128, 256, 48, 32, "bf16"),
+    ("five_on_all", 5, 384, 640, 384, 4, 4, "bf16"),
+    ("eight_on_all", 8, 640, 1152, 768, 6, 6, "bf16"),
     ("mid1", 1, 2048, 1024, 1024, 64, 4, "bf16"),
     ("mid8", 8, 2048, 1024, 1024, 64, 4, "bf16"),
     ("tiny_f32", 5, 256, 128, 128, 8, 2, "f32"),
