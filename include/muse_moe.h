@@ -374,6 +374,21 @@ MUSE_API muse_status muse_int8_matmul(const void* x_codes, const float* x_scales
                                       const muse_int8_weight* w, int64_t N, void* out, int32_t out_dtype, int64_t ldo,
                                       uint32_t* status, void* stream);
 
+/* How a row's scale is made from its largest magnitude. */
+typedef enum muse_int8_scale {
+  MUSE_INT8_SCALE_DIVIDE = 0,     /* max / 127, the float32 division                        */
+  MUSE_INT8_SCALE_RECIPROCAL = 1  /* max * c, c the float32 number next to 1 / 127: what
+                                     PyTorch computes for `amax / 127.0` on a GPU, so that
+                                     the codes equal those of rows quantised there. The
+                                     scales differ from the above by at most one unit in the
+                                     last place (in 4.5 % of the rows), the codes where x / s
+                                     lies that close to n + 1/2                             */
+} muse_int8_scale;
+
+/* muse_quantize_int8_rows with a choice of the scale (muse_int8_scale; the plain form divides). */
+MUSE_API muse_status muse_quantize_int8_rows_scaled(const void* src, int32_t dtype, int64_t rows, int64_t K, int64_t ld,
+                                                    void* codes, float* scales, int32_t scale_rule, void* stream);
+
 /* The same from float rows: x [T, K] of type x_dtype (row t at x + t * ldx) is quantised as by
  * muse_quantize_int8_rows, then multiplied; bit for bit the two calls one after the other.
  * The workspace (device, 256-byte aligned, muse_int8_linear_workspace_size bytes) holds the
@@ -382,6 +397,11 @@ MUSE_API muse_status muse_int8_linear_workspace_size(int64_t T, int64_t K, size_
 MUSE_API muse_status muse_int8_linear(const void* x, int32_t x_dtype, int64_t T, int64_t K, int64_t ldx,
                                       const muse_int8_weight* w, int64_t N, void* out, int32_t out_dtype, int64_t ldo,
                                       void* workspace, size_t workspace_bytes, uint32_t* status, void* stream);
+/* muse_int8_linear with a choice of the rows' scales (muse_int8_scale). */
+MUSE_API muse_status muse_int8_linear_scaled(const void* x, int32_t x_dtype, int64_t T, int64_t K, int64_t ldx,
+                                             const muse_int8_weight* w, int64_t N, void* out, int32_t out_dtype,
+                                             int64_t ldo, void* workspace, size_t workspace_bytes, uint32_t* status,
+                                             int32_t scale_rule, void* stream);
 
 /* ---------------------------------------------------------------------------------
  * The whole layer for a few tokens (cfg->T <= MUSE_FEW_TOKENS) in one kernel: the mathematics

@@ -21,6 +21,7 @@ EXPERTS_DENSE, EXPERTS_NVFP4 = 0, 1
 ACT_BF16, ACT_NVFP4 = 0, 1
 NORM_CENTRED, NORM_INPUT_SCALED = 0, 1
 PROJ_DENSE, PROJ_INT8 = 0, 1
+INT8_SCALE_DIVIDE, INT8_SCALE_RECIPROCAL = 0, 1
 
 STATUS = {0: "MUSE_OK", 1: "MUSE_ERR_INVALID_ARG", 2: "MUSE_ERR_UNSUPPORTED", 3: "MUSE_ERR_WORKSPACE",
           4: "MUSE_ERR_CUDA", 5: "MUSE_ERR_TIMEOUT", 6: "MUSE_ERR_DEVICE"}
@@ -32,7 +33,8 @@ EXPORTS = ("muse_moe_config_init", "muse_latent_moe_workspace_size", "muse_laten
            "muse_selftest_bounded_wait", "muse_quantize_nvfp4_rows", "muse_latent_moe_forward_host_batches",
            "muse_ep_workspace_layout", "muse_ep_dispatch", "muse_ep_experts", "muse_ep_combine",
            "muse_latent_moe_forward_checked", "muse_latent_moe_stage_name", "muse_last_cuda_error",
-           "muse_quantize_int8_rows", "muse_int8_matmul", "muse_int8_linear_workspace_size", "muse_int8_linear",
+           "muse_quantize_int8_rows", "muse_quantize_int8_rows_scaled", "muse_int8_matmul",
+           "muse_int8_linear_workspace_size", "muse_int8_linear", "muse_int8_linear_scaled",
            "muse_latent_moe_few_tokens_workspace_size", "muse_latent_moe_few_tokens",
            "muse_latent_moe_few_tokens_checked", "muse_latent_moe_few_tokens_status")
 
@@ -157,12 +159,16 @@ def lib() -> ctypes.CDLL:
         wp = ctypes.POINTER(Int8Weight)
         L.muse_quantize_int8_rows.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
         L.muse_quantize_int8_rows.restype = ctypes.c_int
+        L.muse_quantize_int8_rows_scaled.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, vp]
+        L.muse_quantize_int8_rows_scaled.restype = ctypes.c_int
         L.muse_int8_matmul.argtypes = [vp, vp, i64, i64, wp, i64, vp, i32, i64, vp, vp]
         L.muse_int8_matmul.restype = ctypes.c_int
         L.muse_int8_linear_workspace_size.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_size_t)]
         L.muse_int8_linear_workspace_size.restype = ctypes.c_int
         L.muse_int8_linear.argtypes = [vp, i32, i64, i64, i64, wp, i64, vp, i32, i64, vp, ctypes.c_size_t, vp, vp]
         L.muse_int8_linear.restype = ctypes.c_int
+        L.muse_int8_linear_scaled.argtypes = L.muse_int8_linear.argtypes[:-1] + [i32, vp]
+        L.muse_int8_linear_scaled.restype = ctypes.c_int
         L.muse_latent_moe_few_tokens_workspace_size.argtypes = [cp, ctypes.POINTER(ctypes.c_size_t)]
         L.muse_latent_moe_few_tokens_workspace_size.restype = ctypes.c_int
         L.muse_latent_moe_few_tokens.argtypes = [cp] + [vp] * 10
@@ -421,10 +427,12 @@ def _one_device(*tensors):
     return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
-def quantize_int8_rows(src, codes=None, scales=None, stream=None):
+def quantize_int8_rows(src, codes=None, scales=None, stream=None, scale_rule: int = INT8_SCALE_DIVIDE):
     """src [rows, K] float32 or bfloat16 (rows may lie apart, K a multiple of 16) -> codes int8
     [rows, K] and scales float32 [rows], created if not given; returns both. For activations a
-    row is a token, for weights [out, in] an output channel."""
+    row is a token, for weights [out, in] an output channel. scale_rule: a row's scale is
+    INT8_SCALE_DIVIDE max / 127, or INT8_SCALE_RECIPROCAL what torch computes for amax / 127.0
+    on a GPU (the codes then equal those of rows quantised with torch)."""
     import torch
     ptr, dtype, ld = _rows(src, "src")
     rows, K = src.shape
@@ -434,20 +442,24 @@ def quantize_int8_rows(src, codes=None, scales=None, stream=None):
     if codes.shape != src.shape:
         raise ValueError("codes must have the shape of src")
     with _one_device(src, codes, scales):
-        _check(lib().muse_quantize_int8_rows(ptr, dtype, int(rows), int(K), ld, _ptr(codes), _ptr(scales),
-                                             _stream_handle(stream)), "muse_quantize_int8_rows")
+        _check(lib().muse_quantize_int8_rows_scaled(ptr, dtype, int(rows), int(K), ld, _ptr(codes), _ptr(scales),
+                                                    int(scale_rule), _stream_handle(stream)),
+               "muse_quantize_int8_rows_scaled")
     return codes, scales
 
 
 class Int8Linear:
     """A product with int8 weights: codes [out, in] and scales [out] (quantize_int8_rows of the
-    weights), for up to T_max rows per call. Holds the workspace of the quantised rows, so calls
+    weights), for up to T_max rows per call; scale_rule says how a row's scale is made (see
+    quantize_int8_rows). Holds the workspace of the quantised rows, so calls
     that overlap on the GPU need holders of their own."""
 
-    def __init__(self, codes, scales, T_max: int):
+    def __init__(self, codes, scales, T_max: int, scale_rule: int = INT8_SCALE_DIVIDE):
         import torch
         _int8_operand(codes, scales, "weight")
-        self.codes, self.scales, self.T_max = codes, scales, int(T_max)
+        if scale_rule not in (INT8_SCALE_DIVIDE, INT8_SCALE_RECIPROCAL):
+            raise ValueError("scale_rule is INT8_SCALE_DIVIDE or INT8_SCALE_RECIPROCAL")
+        self.codes, self.scales, self.T_max, self.scale_rule = codes, scales, int(T_max), int(scale_rule)
         self.N, self.K = (int(n) for n in codes.shape)
         self.weight = Int8Weight(_ptr(codes), _ptr(scales))
         n = ctypes.c_size_t(0)
@@ -488,8 +500,9 @@ class Int8Linear:
             raise ValueError(f"T={T} exceeds T_max={self.T_max}")
 
         def call(optr, odtype, ldo, st):
-            _check(lib().muse_int8_linear(ptr, dtype, T, self.K, ld, self._weight, self.N, optr, odtype, ldo, self._ws,
-                                          self._ws_bytes, self._status, st), "muse_int8_linear")
+            _check(lib().muse_int8_linear_scaled(ptr, dtype, T, self.K, ld, self._weight, self.N, optr, odtype, ldo,
+                                                 self._ws, self._ws_bytes, self._status, self.scale_rule, st),
+                   "muse_int8_linear_scaled")
         return self._run(T, x.device, out, out_dtype or (x.dtype if out is None else None), stream, call)
 
     def matmul(self, x_codes, x_scales, out=None, out_dtype=None, stream=None):

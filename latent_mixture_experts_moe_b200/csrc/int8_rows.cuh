@@ -4,8 +4,11 @@
 //   s_r = max(max_k |x_rk| / 127, 2^-126),   q_rk = x_rk / s_r rounded to nearest, ties to even
 //   out[t, n] = (sum_k q_tk w_nk) * (s_t * v_n)
 //
-// The division is the IEEE float32 one and |q| <= 127 by construction (max |x| / s rounds to
-// at most 127 (1 + 2^-23)). The lower bound on s, the smallest normal float32, gives an
+// The divisions are the IEEE float32 ones, or (MUSE_INT8_SCALE_RECIPROCAL) s_r is max |x| times the
+// float32 number next to 1 / 127, which is how PyTorch evaluates `amax / 127.0` on a GPU. The two
+// scales differ by a unit in the last place in 4.5 % of the rows, and that moves codes whose
+// quotient lies at n + 1/2 (frequent in bf16 rows: 33 codes of 4000 x 8192). |q| <= 127 by
+// construction either way (max |x| / s rounds to at most 127 (1 + 2^-22)). The lower bound on s, the smallest normal float32, gives an
 // all-zero row codes 0 without a special case. A row that holds a NaN or an infinity has no
 // scale: s = NaN, codes 0, so that its products are NaN rather than finite and wrong.
 // The sum is exact in 32-bit integers for K <= 131072 (127^2 K < 2^31); it is rounded once to
@@ -24,9 +27,11 @@ namespace muse {
 constexpr float kInt8ScaleMin = 1.17549435e-38f;  // 2^-126
 
 // The row's scale from the bits of its largest magnitude (as integers they order like the
-// magnitudes, infinity and then NaN last).
-__device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
-  return amax_bits < 0x7f800000u ? fmaxf(__uint_as_float(amax_bits) / 127.0f, kInt8ScaleMin)
+// magnitudes, infinity and then NaN last); reciprocal: see above.
+__device__ __forceinline__ float int8_scale(uint32_t amax_bits, bool reciprocal) {
+  constexpr float kInv127 = 1.0f / 127.0f;
+  const float amax = __uint_as_float(amax_bits);
+  return amax_bits < 0x7f800000u ? fmaxf(reciprocal ? amax * kInv127 : amax / 127.0f, kInt8ScaleMin)
                                  : __int_as_float(0x7fc00000);
 }
 __device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
@@ -99,7 +104,8 @@ struct Int8Load {
 // conversion's instructions bound it (issue slots 68 % busy).
 template <typename T, int TPR, bool ALIGNED>
 __global__ void __launch_bounds__(256, 5) k_quant_rows_int8(const T* __restrict__ src, int64_t ld, int rows, int K,
-                                                         int8_t* __restrict__ codes, float* __restrict__ scales) {
+                                                         int8_t* __restrict__ codes, float* __restrict__ scales,
+                                                         bool reciprocal) {
   constexpr int kVecs = 4;
   __shared__ uint32_t part[8];
   const int sub = threadIdx.x % TPR;
@@ -132,7 +138,7 @@ __global__ void __launch_bounds__(256, 5) k_quant_rows_int8(const T* __restrict_
 #pragma unroll
     for (int w = 0; w < TPR / 32; ++w) amax = max(amax, part[first + w]);
   }
-  const float s = int8_scale(amax), inv = 1.0f / s;
+  const float s = int8_scale(amax, reciprocal), inv = 1.0f / s;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int k = (i * TPR + sub) * 8;
@@ -191,6 +197,7 @@ struct Int8StreamArgs {
   int64_t ldo;
   int T, K, N, stages;
   bool after_quantiser;     // (for the host: how it is launched)
+  bool reciprocal;          // (fused) how the scales are made
   uint32_t* status;
 };
 
@@ -292,7 +299,7 @@ __global__ void __launch_bounds__(Int8Stream<NT, FUSED>::kThreads, 1) k_int8_str
     if (lane == 0) part[wc] = amax;
     sync();
     for (int w = j * per; w < (j + 1) * per; ++w) amax = max(amax, part[w]);
-    const float s = int8_scale(amax), inv = 1.0f / s;
+    const float s = int8_scale(amax, p.reciprocal), inv = 1.0f / s;
     if (j < T) {
       if (sub == 0) xs[j] = s;
       uint8_t* q = smem + S::kRedBytes + j * S::xstride(K);

@@ -545,7 +545,7 @@ bool valid_dtype(int32_t dtype) { return dtype == MUSE_F32 || dtype == MUSE_BF16
 
 template <typename T>
 muse_status quantize_int8_t(const T* src, int64_t rows, int64_t K, int64_t ld, int8_t* codes, float* scales,
-                            cudaStream_t st) {
+                            int32_t rule, cudaStream_t st) {
   const bool aligned = aligned16(src) && (rows == 1 || ld * static_cast<int64_t>(sizeof(T)) % 16 == 0);
   const int n = static_cast<int>(rows), k = static_cast<int>(K);
   // as many threads as hold the row at 32 values each, at most a block
@@ -553,16 +553,17 @@ muse_status quantize_int8_t(const T* src, int64_t rows, int64_t K, int64_t ld, i
   auto kern = tpr == 32    ? (aligned ? k_quant_rows_int8<T, 32, true> : k_quant_rows_int8<T, 32, false>)
               : tpr == 128 ? (aligned ? k_quant_rows_int8<T, 128, true> : k_quant_rows_int8<T, 128, false>)
                            : (aligned ? k_quant_rows_int8<T, 256, true> : k_quant_rows_int8<T, 256, false>);
-  kern<<<static_cast<unsigned>(cdiv(rows, 256 / tpr)), 256, 0, st>>>(src, ld, n, k, codes, scales);
+  kern<<<static_cast<unsigned>(cdiv(rows, 256 / tpr)), 256, 0, st>>>(src, ld, n, k, codes, scales,
+                                                                       rule == MUSE_INT8_SCALE_RECIPROCAL);
   MUSE_CK(cudaGetLastError());
   return MUSE_OK;
 }
 
 muse_status quantize_int8(const void* src, int32_t dtype, int64_t rows, int64_t K, int64_t ld, void* codes,
-                          float* scales, cudaStream_t st) {
+                          float* scales, int32_t rule, cudaStream_t st) {
   int8_t* c = static_cast<int8_t*>(codes);
-  return dtype == MUSE_BF16 ? quantize_int8_t(static_cast<const __nv_bfloat16*>(src), rows, K, ld, c, scales, st)
-                            : quantize_int8_t(static_cast<const float*>(src), rows, K, ld, c, scales, st);
+  return dtype == MUSE_BF16 ? quantize_int8_t(static_cast<const __nv_bfloat16*>(src), rows, K, ld, c, scales, rule, st)
+                            : quantize_int8_t(static_cast<const float*>(src), rows, K, ld, c, scales, rule, st);
 }
 
 // How an int8 product of many rows is tiled: on CTA pairs (256 mt features x tokens), or with K
@@ -727,7 +728,7 @@ Int8StreamArgs int8_stream_args(const void* x, int64_t ldx, const float* xs, int
                                 const muse_int8_weight& w, int64_t N, void* out, int64_t ldo, uint32_t* status,
                                 bool after_quantiser) {
   return {x, ldx, xs, static_cast<const int8_t*>(w.codes), w.scales, out, ldo, static_cast<int>(T),
-          static_cast<int>(K), static_cast<int>(N), 0, after_quantiser, status};
+          static_cast<int>(K), static_cast<int>(N), 0, after_quantiser, false, status};
 }
 
 // after_quantiser: the codes' quantiser was launched just before on the stream
@@ -754,8 +755,10 @@ bool int8_fused(const void* x, int32_t dtype, int64_t T, int64_t K, int64_t ldx)
 
 template <typename TX>
 muse_status int8_linear_fused(const void* x, int64_t ldx, int64_t T, int64_t K, const muse_int8_weight& w, int64_t N,
-                              void* out, int32_t out_dtype, int64_t ldo, uint32_t* status, cudaStream_t st) {
+                              void* out, int32_t out_dtype, int64_t ldo, int32_t rule, uint32_t* status,
+                              cudaStream_t st) {
   Int8StreamArgs a = int8_stream_args(x, ldx, nullptr, T, K, w, N, out, ldo, status, false);
+  a.reciprocal = rule == MUSE_INT8_SCALE_RECIPROCAL;
   return out_dtype == MUSE_BF16 ? launch_int8_stream<1, true, TX, __nv_bfloat16>(a, st)
                                 : launch_int8_stream<1, true, TX, float>(a, st);
 }
@@ -894,7 +897,7 @@ muse_status int8_projection(Pass<T>& p, const void* rows, int64_t K, const void*
   const muse_int8_weight& w = *static_cast<const muse_int8_weight*>(W);
   uint8_t* codes = p.at(p.lay.proj_codes);
   float* scales = p.template ptr<float>(p.lay.proj_scales);
-  MUSE_TRY(quantize_int8(rows, p.c.dtype, p.c.T, K, K, codes, scales, p.st));
+  MUSE_TRY(quantize_int8(rows, p.c.dtype, p.c.T, K, K, codes, scales, MUSE_INT8_SCALE_DIVIDE, p.st));
   MUSE_CK(p.mark());
   const bool next = p.events == nullptr;  // (nothing between the two launches)
   if (sq.ss != nullptr)
@@ -1571,6 +1574,8 @@ bool int8_out_overlaps(const void* out, int64_t T, int64_t N, int32_t out_dtype,
          rows_overlap(out, T, N * size, ldo * size, w.scales, 1, 4 * N, 4 * N);
 }
 
+bool valid_scale_rule(int32_t rule) { return rule == MUSE_INT8_SCALE_DIVIDE || rule == MUSE_INT8_SCALE_RECIPROCAL; }
+
 // the sizes, weights and output of an int8 product
 muse_status validate_int8(int64_t T, int64_t K, const muse_int8_weight* w, int64_t N, const void* out,
                           int32_t out_dtype, int64_t ldo, const uint32_t* status) {
@@ -1876,6 +1881,12 @@ muse_status muse_quantize_nvfp4_rows(const void* src, int64_t rows, int64_t K, v
 
 muse_status muse_quantize_int8_rows(const void* src, int32_t dtype, int64_t rows, int64_t K, int64_t ld, void* codes,
                                     float* scales, void* stream) {
+  return muse_quantize_int8_rows_scaled(src, dtype, rows, K, ld, codes, scales, MUSE_INT8_SCALE_DIVIDE, stream);
+}
+
+muse_status muse_quantize_int8_rows_scaled(const void* src, int32_t dtype, int64_t rows, int64_t K, int64_t ld,
+                                           void* codes, float* scales, int32_t scale_rule, void* stream) {
+  if (!valid_scale_rule(scale_rule)) return MUSE_ERR_INVALID_ARG;
   if (!valid_dtype(dtype) || rows < 0 || K < 16 || K % 16 != 0 || ld < K) return MUSE_ERR_INVALID_ARG;
   if (rows > (int64_t(1) << 30) || K > (int64_t(1) << 20) || ld > (int64_t(1) << 40)) return MUSE_ERR_UNSUPPORTED;
   if (rows == 0) return MUSE_OK;
@@ -1885,7 +1896,7 @@ muse_status muse_quantize_int8_rows(const void* src, int32_t dtype, int64_t rows
   if (rows_overlap(src, rows, K * size, ld * size, codes, 1, rows * K, rows * K) ||
       rows_overlap(src, rows, K * size, ld * size, scales, 1, 4 * rows, 4 * rows))
     return MUSE_ERR_INVALID_ARG;
-  return quantize_int8(src, dtype, rows, K, ld, codes, scales, static_cast<cudaStream_t>(stream));
+  return quantize_int8(src, dtype, rows, K, ld, codes, scales, scale_rule, static_cast<cudaStream_t>(stream));
 }
 
 muse_status muse_int8_matmul(const void* x_codes, const float* x_scales, int64_t T, int64_t K,
@@ -1912,6 +1923,15 @@ muse_status muse_int8_linear_workspace_size(int64_t T, int64_t K, size_t* bytes)
 muse_status muse_int8_linear(const void* x, int32_t x_dtype, int64_t T, int64_t K, int64_t ldx,
                              const muse_int8_weight* w, int64_t N, void* out, int32_t out_dtype, int64_t ldo,
                              void* workspace, size_t workspace_bytes, uint32_t* status, void* stream) {
+  return muse_int8_linear_scaled(x, x_dtype, T, K, ldx, w, N, out, out_dtype, ldo, workspace, workspace_bytes, status,
+                                 MUSE_INT8_SCALE_DIVIDE, stream);
+}
+
+muse_status muse_int8_linear_scaled(const void* x, int32_t x_dtype, int64_t T, int64_t K, int64_t ldx,
+                                    const muse_int8_weight* w, int64_t N, void* out, int32_t out_dtype, int64_t ldo,
+                                    void* workspace, size_t workspace_bytes, uint32_t* status, int32_t scale_rule,
+                                    void* stream) {
+  if (!valid_scale_rule(scale_rule)) return MUSE_ERR_INVALID_ARG;
   MUSE_TRY(validate_int8(T, K, w, N, out, out_dtype, ldo, status));
   if (!valid_dtype(x_dtype) || ldx < K) return MUSE_ERR_INVALID_ARG;
   if (ldx > (int64_t(1) << 40)) return MUSE_ERR_UNSUPPORTED;
@@ -1925,10 +1945,10 @@ muse_status muse_int8_linear(const void* x, int32_t x_dtype, int64_t T, int64_t 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (int8_fused(x, x_dtype, T, K, ldx))
     return x_dtype == MUSE_BF16
-               ? int8_linear_fused<__nv_bfloat16>(x, ldx, T, K, *w, N, out, out_dtype, ldo, status, st)
-               : int8_linear_fused<float>(x, ldx, T, K, *w, N, out, out_dtype, ldo, status, st);
+               ? int8_linear_fused<__nv_bfloat16>(x, ldx, T, K, *w, N, out, out_dtype, ldo, scale_rule, status, st)
+               : int8_linear_fused<float>(x, ldx, T, K, *w, N, out, out_dtype, ldo, scale_rule, status, st);
   float* scales = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align_up(static_cast<size_t>(T * K), kAlign));
-  MUSE_TRY(quantize_int8(x, x_dtype, T, K, ldx, workspace, scales, st));
+  MUSE_TRY(quantize_int8(x, x_dtype, T, K, ldx, workspace, scales, scale_rule, st));
   return int8_product(workspace, scales, T, K, *w, N, out, out_dtype, ldo, status, true, st);
 }
 
