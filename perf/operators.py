@@ -141,7 +141,7 @@ def _int8_state(case, seed):
         s["x_codes"], s["x_scales"] = q.to(torch.int8), sx[:, 0].contiguous()
     if own:
         import latent_mixture_experts_moe_b200 as moe
-        s["linear"] = moe.Int8Linear(s["w_codes"], s["w_scales"], T_max=T)
+        s["linear"] = moe.Int8Linear(s["w_codes"], s["w_scales"], T_max=T, scale_rule=moe.INT8_SCALE_RECIPROCAL)
     return s
 
 
