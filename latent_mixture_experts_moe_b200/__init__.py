@@ -83,12 +83,21 @@ class Tensor(ctypes.Structure):
 ELEM_F32, ELEM_BF16, ELEM_U8, ELEM_I8 = 0, 1, 2, 3
 
 
+_elem_types: Dict = {}
+
+
 def tensor_desc(t) -> Tensor:
     """The muse_tensor of a torch tensor (its own shape and strides: a non-contiguous view
     is described as it is, and the library rejects it)."""
-    import torch
-    elem = {torch.float32: ELEM_F32, torch.bfloat16: ELEM_BF16, torch.uint8: ELEM_U8, torch.int8: ELEM_I8}.get(t.dtype, -1)
-    return Tensor(t.data_ptr(), elem, t.dim(), tuple(t.shape[:3]), tuple(t.stride()[:3]))
+    if not _elem_types:
+        import torch
+        _elem_types.update({torch.float32: ELEM_F32, torch.bfloat16: ELEM_BF16, torch.uint8: ELEM_U8,
+                            torch.int8: ELEM_I8})
+    dim = t.dim()
+    n = min(dim, 3)
+    d = Tensor(t.data_ptr(), _elem_types.get(t.dtype, -1), dim)
+    d.shape[:n], d.stride[:n] = t.shape[:n], t.stride()[:n]
+    return d
 
 
 class Nvfp4Weight(ctypes.Structure):
@@ -601,20 +610,21 @@ class LatentMoE:
     W_pool_scales, W_unpool_codes and W_unpool_scales instead, of quantize_int8_rows); router_bias, pre_norm_gain and the
     feed-forward sublayer's ffn_pre_gain, ffn_post_gain and residual_gate (float32) are
     optional. modes: make_config keywords (router_mode, norm_mode, gamma_shared, ...).
+    Every call computes with what the entries of self.w hold then, so weights may be changed in
+    place or replaced (by tensors of the same shapes) between calls.
     """
+
+    OPTIONS = ("router_bias", "pre_norm_gain", "ffn_pre_gain", "ffn_post_gain", "residual_gate")
 
     def __init__(self, weights: Dict, T_max: int, k: int, eps: float = 1e-6, **modes):
         import torch
         self.w = dict(weights)
         E, D = weights["W_router"].shape
         I, L, self.nvfp4 = expert_weight_dims(weights)
-        # the expert tensors as the shape-checked entry point takes them
-        self.experts = tuple((weights[n + "_codes"], weights[n + "_scales"], weights[n + "_mscale"]) if self.nvfp4
-                             else weights[n] for n in ("W_gate", "W_up", "W_down"))
+        # experts and projections as the C ABI takes them
         self.w["W_gate"], self.w["W_up"], self.w["W_down"] = expert_operands(weights, self.nvfp4)
-        # the projections as the C ABI and as the shape-checked entry points take them
-        self.w["W_pool"], self.pool = projection_operand(weights, "W_pool")
-        self.w["W_unpool"], self.unpool = projection_operand(weights, "W_unpool")
+        for name in ("W_pool", "W_unpool"):
+            self.w[name], _ = projection_operand(weights, name)
         self.dtype = {torch.float32: "f32", torch.bfloat16: "bf16"}[weights["W_router"].dtype]
         self.dims = dict(D=int(D), L=L, I=I, E=int(E), k=k, eps=eps)
         self.modes = modes
@@ -630,11 +640,34 @@ class LatentMoE:
         except MuseError as e:
             if e.code != 2:  # MUSE_ERR_UNSUPPORTED
                 raise
-        # its configuration and the weights' descriptors, once: a call of a few microseconds would
-        # otherwise spend more time on marshalling than on the GPU
-        self._few_config = self.config(min(T_max, FEW_TOKENS), self.few_workspace)
-        self._few_weights = _weight_descs(weights["W_router"], self.pool, *self.experts, weights["gamma"],
-                                          self.unpool)
+        self._few_key = self._few_call = None
+
+    def operands(self):
+        """W_router, W_pool, W_gate, W_up, W_down, gamma and W_unpool as the shape-checked entry points
+        take them: tensors, or tuples of NVFP4 and int8 parts."""
+        w = self.w
+
+        def one(name, parts):
+            return tuple(w[name + p] for p in parts) if name + "_codes" in w else w[name]
+        experts = (one(n, ("_codes", "_scales", "_mscale")) for n in ("W_gate", "W_up", "W_down"))
+        return (w["W_router"], one("W_pool", ("_codes", "_scales")), *experts, w["gamma"],
+                one("W_unpool", ("_codes", "_scales")))
+
+    def _few(self):
+        """Configuration and weight descriptors of few_tokens. They are made again only when something
+        they say has changed (2 us to find out): a call of a few microseconds would otherwise
+        spend more time on marshalling than on the GPU."""
+        w, ws = self.w, self.few_workspace
+        key = ([(t.data_ptr(), t.shape, t.dtype, t.is_contiguous()) if hasattr(t, "data_ptr") else None
+                for t in w.values()],
+               list(w), list(self.dims.values()), dict(self.modes), ws is not None and (ws.data_ptr(), ws.numel()))
+        if key != self._few_key:
+            operands = self.operands()
+            options = [w[n] for n in self.OPTIONS if w.get(n) is not None]
+            _one_device(*options, *(t for o in operands for t in (o if type(o) is tuple else (o,))))
+            self._few_call = self.config(min(self.T_max, FEW_TOKENS), ws), _weight_descs(*operands)
+            self._few_key = key
+        return self._few_call
 
     def config(self, T: int, workspace=None) -> Config:
         return block_config(T, self.dims, self.dtype, self.modes, self.w, self.nvfp4, workspace)
@@ -651,8 +684,7 @@ class LatentMoE:
             cfg.stage_events = ctypes.cast(stage_events, ctypes.c_void_p)
         if out is None:
             out = torch.empty((T, self.dims["D"]), dtype=x.dtype, device=x.device)
-        w = self.w
-        forward_checked(cfg, x, w["W_router"], self.pool, *self.experts, w["gamma"], self.unpool, out, stream)
+        forward_checked(cfg, x, *self.operands(), out, stream)
         return out
 
     def few_tokens(self, x, out=None, stream=None, topk_idx=None, topk_w=None):
@@ -663,18 +695,20 @@ class LatentMoE:
         T = x.shape[0]
         if T > min(self.T_max, FEW_TOKENS):
             raise ValueError(f"T={T} exceeds {min(self.T_max, FEW_TOKENS)}")
-        for t, dtype in ((topk_idx, torch.int32), (topk_w, torch.float32)):
+        routing = () if topk_idx is None and topk_w is None else ((topk_idx, torch.int32), (topk_w, torch.float32))
+        for t, dtype in routing:
             if t is not None and (t.shape != (T, self.dims["k"]) or t.dtype != dtype or t.device != x.device
                                   or not t.is_contiguous()):
                 raise ValueError(f"topk_idx and topk_w are contiguous [{T}, {self.dims['k']}] int32 and float32 tensors "
                                  "on x's device")
         with _one_device(x, self.w["W_router"], x if out is None else out):
-            cfg = Config.from_buffer_copy(self._few_config)
+            few_config, weights = self._few()
+            cfg = Config.from_buffer_copy(few_config)
             cfg.T, cfg.topk_idx_out, cfg.topk_w_out = T, _ptr(topk_idx), _ptr(topk_w)
             if out is None:
                 out = torch.empty((T, self.dims["D"]), dtype=x.dtype, device=x.device)
             code = lib().muse_latent_moe_few_tokens_checked(
-                ctypes.byref(cfg), ctypes.byref(tensor_desc(x)), *self._few_weights, ctypes.byref(tensor_desc(out)),
+                ctypes.byref(cfg), ctypes.byref(tensor_desc(x)), *weights, ctypes.byref(tensor_desc(out)),
                 _stream_handle(stream))
             _check(code, "muse_latent_moe_few_tokens_checked")
         return out
