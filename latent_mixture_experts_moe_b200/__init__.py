@@ -406,14 +406,18 @@ def quantize_nvfp4_rows(src, codes, scales, stream=None) -> None:
                                           _stream_handle(stream)), "muse_quantize_nvfp4_rows")
 
 
+_float_types: Dict = {}
+
+
 def _rows(t, name: str):
     """Pointer, muse_dtype and row distance of a 2-D float tensor whose rows are contiguous."""
-    import torch
-    dtype = MUSE_BF16 if t.dtype is torch.bfloat16 else MUSE_F32 if t.dtype is torch.float32 else -1
-    if dtype < 0 or t.dim() != 2:
+    if not _float_types:
+        import torch
+        _float_types.update({torch.bfloat16: MUSE_BF16, torch.float32: MUSE_F32})
+    dtype, strides = _float_types.get(t.dtype), t.stride()
+    if dtype is None or len(strides) != 2:
         raise ValueError(f"{name} must be a 2-D float32 or bfloat16 tensor")
-    rows, cols = t.shape
-    step, inner = t.stride()
+    (rows, cols), (step, inner) = t.shape, strides
     if inner != 1 and cols > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
     return t.data_ptr(), dtype, step if rows > 1 else cols
@@ -460,7 +464,8 @@ def quantize_int8_rows(src, codes=None, scales=None, stream=None, scale_rule: in
 class Int8Linear:
     """A product with int8 weights: codes [out, in] and scales [out] (quantize_int8_rows of the
     weights), for up to T_max rows per call; scale_rule says how a row's scale is made (see
-    quantize_int8_rows). Holds the workspace of the quantised rows, so calls
+    quantize_int8_rows). The weights may be changed in place or replaced (self.codes, self.scales, by
+    tensors of the same shapes) between calls. Holds the workspace of the quantised rows, so calls
     that overlap on the GPU need holders of their own."""
 
     def __init__(self, codes, scales, T_max: int, scale_rule: int = INT8_SCALE_DIVIDE):
@@ -471,6 +476,8 @@ class Int8Linear:
         self.codes, self.scales, self.T_max, self.scale_rule = codes, scales, int(T_max), int(scale_rule)
         self.N, self.K = (int(n) for n in codes.shape)
         self.weight = Int8Weight(_ptr(codes), _ptr(scales))
+        self._linear = lib().muse_int8_linear_scaled
+        self._weight_key = self._key()
         n = ctypes.c_size_t(0)
         _check(lib().muse_int8_linear_workspace_size(self.T_max, self.K, ctypes.byref(n)),
                "muse_int8_linear_workspace_size")
@@ -482,16 +489,31 @@ class Int8Linear:
         self._weight = ctypes.byref(self.weight)
         self._ws, self._ws_bytes, self._status = _ptr(self.workspace), self.workspace.numel(), _ptr(self.status)
 
+    def _key(self):
+        c, s = self.codes, self.scales
+        return (c.data_ptr(), s.data_ptr(), c.shape, s.shape, c.dtype, s.dtype, c.is_contiguous(), s.is_contiguous())
+
     def _run(self, T, device, out, out_dtype, stream, call):
         """call(out pointer, its muse_dtype and row distance, stream handle) on the holder's device."""
         torch = self._torch
+        if self._key() != self._weight_key:  # the weights were replaced
+            _int8_operand(self.codes, self.scales, "weight")
+            if tuple(self.codes.shape) != (self.N, self.K):
+                raise ValueError(f"the weights' codes must be [{self.N}, {self.K}]")
+            if any(t.device != self._device for t in (self.codes, self.scales)):
+                raise ValueError(f"tensors must be on {self._device}")
+            self.weight.codes, self.weight.scales = _ptr(self.codes), _ptr(self.scales)
+            self._weight_key = self._key()
         if device != self._device or (out is not None and out.device != device):
             raise ValueError(f"tensors must be on {self._device}")
+        dtype = None
         if out is None:
             out = torch.empty((T, self.N), dtype=out_dtype, device=device)
+            ptr, dtype, ld = out.data_ptr(), _float_types.get(out_dtype), self.N
         elif tuple(out.shape) != (T, self.N) or (out_dtype is not None and out.dtype != out_dtype):
             raise ValueError(f"out must be [{T}, {self.N}] of the output type")
-        ptr, dtype, ld = _rows(out, "out")
+        if dtype is None:
+            ptr, dtype, ld = _rows(out, "out")
         if torch.cuda.current_device() == device.index:
             call(ptr, dtype, ld, _stream_handle(stream))
         else:
@@ -509,9 +531,8 @@ class Int8Linear:
             raise ValueError(f"T={T} exceeds T_max={self.T_max}")
 
         def call(optr, odtype, ldo, st):
-            _check(lib().muse_int8_linear_scaled(ptr, dtype, T, self.K, ld, self._weight, self.N, optr, odtype, ldo,
-                                                 self._ws, self._ws_bytes, self._status, self.scale_rule, st),
-                   "muse_int8_linear_scaled")
+            _check(self._linear(ptr, dtype, T, self.K, ld, self._weight, self.N, optr, odtype, ldo, self._ws,
+                                self._ws_bytes, self._status, self.scale_rule, st), "muse_int8_linear_scaled")
         return self._run(T, x.device, out, out_dtype or (x.dtype if out is None else None), stream, call)
 
     def matmul(self, x_codes, x_scales, out=None, out_dtype=None, stream=None):

@@ -118,3 +118,39 @@ def test_replacements_that_do_not_fit_are_refused():
         layer.few_tokens(x)
     layer.w["gamma"] = kept["gamma"]
     assert bool(torch.isfinite(layer.few_tokens(x)).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("how", ["attribute", "storage"])
+@pytest.mark.parametrize("T", [3, 40])
+def test_replaced_weights_of_a_product_are_used(T, how):
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    a, b = (moe.quantize_int8_rows(torch.randn(96, 128, device="cuda", generator=gen)) for _ in range(2))
+    x = torch.randn(T, 128, device="cuda", generator=gen)
+    lin = moe.Int8Linear(a[0].clone(), a[1].clone(), T_max=T)
+    lin(x)
+    old = [lin.codes.data, lin.scales.data]
+    if how == "attribute":
+        lin.codes, lin.scales = b
+    else:
+        lin.codes.data, lin.scales.data = b[0].clone(), b[1].clone()
+    other = moe.Int8Linear(*b, T_max=T)
+    assert torch.equal(lin(x), other(x))
+    xc, xs = moe.quantize_int8_rows(x)
+    assert torch.equal(lin.matmul(xc, xs), other.matmul(xc, xs))
+    del old
+
+
+@pytest.mark.gpu
+def test_replacements_that_do_not_fit_a_product_are_refused():
+    codes, scales = moe.quantize_int8_rows(torch.randn(64, 128, device="cuda"))
+    lin = moe.Int8Linear(codes, scales, T_max=4)
+    x = torch.randn(4, 128, device="cuda")
+    good = lin(x)
+    for bad in ((codes[:, :64], scales), (codes[:32], scales[:32]), (codes, scales[:32]), (codes.float(), scales),
+                (codes, scales.cpu()), (codes.cpu(), scales)):
+        lin.codes, lin.scales = bad
+        with pytest.raises(ValueError):
+            lin(x)
+    lin.codes, lin.scales = codes, scales
+    assert torch.equal(lin(x), good)
