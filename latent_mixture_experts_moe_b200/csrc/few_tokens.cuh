@@ -12,7 +12,8 @@
 //   4  c = sum_j g_j y_j / rms_j (1 + gamma)
 //   5  out = W_unpool c
 //   6  post norm and residual gate                        (only with those)
-// y and the sublayer's f stay FP32; z, h and c are stored in the type the next product
+// y, the sublayer's f and a latent that a norm follows stay FP32 (raw, it may lie outside f16's
+// range, from which the norm brings it back); z, h and c are stored in the type the next product
 // reads (bf16; f16 for NVFP4 experts, whose decoded weights are f16; float32). bf16 products of
 // intermediates carry a token as two bf16 numbers, the rounded value and what rounding took off
 // (16 significant bits): up to four tokens in the MMA's eight columns, which would otherwise be
@@ -150,6 +151,7 @@ struct FewArgs {
   // workspace
   uint32_t *status, *barrier;
   float *logits, *y, *ss, *f, *ssf;
+  float* zraw;            // the latent before its norm (with pre_norm_gain)
   void *xn, *z, *h, *c;
 };
 
@@ -862,11 +864,6 @@ __device__ __forceinline__ void few_put(T* a, int64_t second, int64_t i, float v
     a[second + i] = from_f32<T>(fabsf(rest) < INFINITY ? rest : 0.0f);  // (infinities and NaN stay what they are)
   }
 }
-template <typename T>
-__device__ __forceinline__ float few_get(const T* a, int64_t second, int64_t i) {
-  if constexpr (std::is_same<T, __nv_bfloat16>::value) return to_f32(a[i]) + to_f32(a[second + i]);
-  return to_f32(a[i]);
-}
 
 __device__ __forceinline__ float few_silu(float a) { return a / (1.0f + expf(-a)); }
 
@@ -1058,8 +1055,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_cons
           routed = true;
         } else if (routed || __all_sync(0xffffffffu, *abort != 0 || mbar_try_wait(red.full(), red.phase))) {
           chunk(c, FEW_POOL, T, [&](const FewChunks& cc, int j, float v) {
-            if (lane < cc.len)
-              few_put(static_cast<TZ*>(p.z), static_cast<int64_t>(T) * L, static_cast<int64_t>(j) * L + cc.f + lane, v);
+            const int64_t o = static_cast<int64_t>(j) * L + cc.f + lane;
+            if (lane < cc.len && zn) p.zraw[o] = v;
+            else if (lane < cc.len) few_put(static_cast<TZ*>(p.z), static_cast<int64_t>(T) * L, o, v);
           });
           c.next();
         }
@@ -1166,7 +1164,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few_tokens(const __grid_cons
         for (int t = blockIdx.x; t < T; t += gridDim.x)
           few_norm_row(
               static_cast<const TA*>(p.pre_norm_gain), L, p.pre_norm_eps, part, tid,
-              [&](int i) { return few_get(z, static_cast<int64_t>(T) * L, static_cast<int64_t>(t) * L + i); },
+              [&](int i) { return __ldcg(p.zraw + static_cast<int64_t>(t) * L + i); },
               [&](int i, float v) { few_put(z, static_cast<int64_t>(T) * L, static_cast<int64_t>(t) * L + i, v); });
         arrive(FEW_ZN);
       }

@@ -1425,7 +1425,7 @@ muse_status check_tensors(const muse_moe_config& c, const muse_tensor* x, const 
 // call), then the intermediates.
 constexpr size_t kFewHeader = 128 * (1 + kFewBarriers);
 struct FewLayout {
-  size_t logits, xn, z, h, y, ss, c, f, ssf, total;
+  size_t logits, xn, zraw, z, h, y, ss, c, f, ssf, total;
 };
 
 muse_status validate_few(const muse_moe_config* c) {
@@ -1448,6 +1448,7 @@ FewLayout few_layout(const muse_moe_config& c) {
   };
   l.logits = take(sizeof(float) * T * c.E);
   l.xn = take(c.ffn_pre_gain != nullptr ? as * T * c.D : 0);
+  l.zraw = take(c.pre_norm_gain != nullptr ? sizeof(float) * T * c.L : 0);
   // (4 bytes each: float32, or two bf16 numbers)
   l.z = take(4 * T * c.L);
   l.h = take(4 * A * c.I);
@@ -1528,6 +1529,7 @@ muse_status few_tokens_impl(const muse_moe_config& c, const void* x, const void*
   a.y = reinterpret_cast<float*>(ws + l.y);
   a.ss = reinterpret_cast<float*>(ws + l.ss);
   a.f = reinterpret_cast<float*>(ws + l.f);
+  a.zraw = reinterpret_cast<float*>(ws + l.zraw);
   a.ssf = reinterpret_cast<float*>(ws + l.ssf);
   a.xn = ws + l.xn;
   a.z = ws + l.z;
