@@ -345,7 +345,7 @@ MUSE_API muse_status muse_quantize_nvfp4_rows(const void* src, int64_t rows, int
  * channel's weights), and their product:
  *   s_r = max(max_k |x_rk| / 127, 2^-126),  q_rk = x_rk / s_r rounded to nearest, ties to even
  *   out[t, n] = (sum_k q_tk w_nk) * (s_t * v_n)
- * max / 127 and x / s are float32 divisions; the sum is exact (K <= 131072), rounded to
+ * max / 127 and x / s are float32 divisions; the sum is exact (K <= 131072, any codes), rounded to
  * float32, multiplied by the float32 product of the scales and rounded to the output type.
  * A row holding a NaN or an infinity gets scale NaN and codes 0: its products are NaN.
  * Codes and weights are dense row-major; x and out rows may lie further apart (ld, in

@@ -109,6 +109,12 @@ struct ElemTraits<float> {
 
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(float v) { return v; }
+// A 32-bit sum of at most 131072 products of 8-bit integers, modulo 2^32, rounded to float32. The
+// sums lie between -2^31 + 2^24 and 2^31; only the last (all codes -128) does not fit a signed
+// integer, and its bits, those of -2^31, stand for no other sum.
+__device__ __forceinline__ float int8_sum(uint32_t s) {
+  return s == 0x80000000u ? 2147483648.0f : static_cast<float>(static_cast<int32_t>(s));
+}
 template <typename T>
 __device__ __forceinline__ T from_f32(float v);
 template <>

@@ -448,6 +448,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               yv[i] = acc_value<TIn>(v[i], __shfl_sync(0xffffffffu, xs, i) * wscale[h]);
+            // 2^31 (see int8_sum; looked for only where K reaches it: 1 % of 8192 x 4096 x 8192)
+            if (p.k_blocks >= 1024) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) yv[i] = v[i] == 0x80000000u ? -yv[i] : yv[i];
+            }
           }
           emit(yv, c, col_cta + h * 256, row0, n, fok[h], col_cta + h * 256 + fl);
           if constexpr (EPI == EPI_STORE_SS) {

@@ -11,7 +11,7 @@
 // construction either way (max |x| / s rounds to at most 127 (1 + 2^-22)). The lower bound on s, the smallest normal float32, gives an
 // all-zero row codes 0 without a special case. A row that holds a NaN or an infinity has no
 // scale: s = NaN, codes 0, so that its products are NaN rather than finite and wrong.
-// The sum is exact in 32-bit integers for K <= 131072 (127^2 K < 2^31); it is rounded once to
+// The sum is exact in 32-bit integers for K <= 131072 (int8_sum); it is rounded once to
 // float32, multiplied by the product of the scales and rounded to the output type.
 #pragma once
 
@@ -369,12 +369,12 @@ __global__ void __launch_bounds__(Int8Stream<NT, FUSED>::kThreads, 1) k_int8_str
           mine[(8 * n + 2 * t + (i & 1)) * 33 + 16 * m + 8 * (i >> 1) + g] = acc[m][n][i];
     sync();
     for (int j = wc; j < T; j += 8) {
-      int v = 0;
+      uint32_t v = 0;
 #pragma unroll
       for (int q = 0; q < 8; ++q) v += red[(q * 16 + j) * 33 + lane];
       if (lane < c.len)
         static_cast<TOut*>(p.out)[static_cast<int64_t>(j) * p.ldo + c.f + lane] =
-            from_f32<TOut>(static_cast<float>(v) * (xs[j] * p.w_scale[c.f + lane]));
+            from_f32<TOut>(int8_sum(v) * (xs[j] * p.w_scale[c.f + lane]));
     }
     sync();
   }

@@ -33,9 +33,9 @@ struct Int8SplitShape {
   static_assert(BN * 128u * 4u <= kStages * kStageBytes, "the partial sums reuse the ring");
 };
 
-__device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+__device__ __forceinline__ uint4 ld_cluster_uint4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
 
@@ -150,17 +150,17 @@ __global__ void __launch_bounds__(192, 1) k_int8_splitk(const __grid_constant__ 
 #pragma unroll
   for (int i = 0; i < 4; ++i) ws[i] = f + i < p.N ? p.w_scale[f + i] : 0.0f;
   for (int j = rank + splits * warp; j < n; j += splits * 6) {
-    int4 v = make_int4(0, 0, 0, 0);
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
     for (int r = 0; r < splits; ++r) {
-      const int4 u = ld_cluster_int4(mapa_shared(smem_u32(part + j * 128 + 4 * lane), static_cast<uint32_t>(r)));
+      const uint4 u = ld_cluster_uint4(mapa_shared(smem_u32(part + j * 128 + 4 * lane), static_cast<uint32_t>(r)));
       v.x += u.x;
       v.y += u.y;
       v.z += u.z;
       v.w += u.w;
     }
     const float xs = p.x_scale[row0 + j];
-    const float y[4] = {static_cast<float>(v.x) * (xs * ws[0]), static_cast<float>(v.y) * (xs * ws[1]),
-                        static_cast<float>(v.z) * (xs * ws[2]), static_cast<float>(v.w) * (xs * ws[3])};
+    const float y[4] = {int8_sum(v.x) * (xs * ws[0]), int8_sum(v.y) * (xs * ws[1]),
+                        int8_sum(v.z) * (xs * ws[2]), int8_sum(v.w) * (xs * ws[3])};
     TOut* out = static_cast<TOut*>(p.out) + (static_cast<int64_t>(row0) + j) * p.ldo + f;
     // four at once where the address allows it
     if (f + 4 <= p.N && (reinterpret_cast<uintptr_t>(out) & (4 * sizeof(TOut) - 1)) == 0) {
