@@ -4,6 +4,12 @@ Argument marshalling only: every step of the block runs in the library's CUDA ke
 PyTorch tensors are accepted as containers of device memory (their data pointers are
 passed through the C ABI declared in include/muse_moe.h); nothing here computes.
 If the compiled library is missing, importing works but every call raises.
+
+Calls take stream= (a torch.cuda.Stream or a raw handle; by default the current stream). What
+they return is memory of that stream, as if they were made under torch.cuda.stream(stream); the
+caller orders the stream after the work that makes their inputs (and after the holder's
+construction), and other streams after it (wait_stream; record_stream where a tensor's last use
+is on another stream).
 """
 from __future__ import annotations
 
@@ -257,6 +263,19 @@ def _stream_handle(stream) -> int:
     return int(getattr(stream, "cuda_stream", stream))
 
 
+def _empty(shape, dtype, device, stream):
+    """An output in memory of the stream that the call runs on: memory of another one may still be
+    in use by work that is pending there."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_handle(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def forward(cfg: Config, x, W_router, W_pool, W_gate, W_up, W_down, gamma, W_unpool, out, stream=None) -> None:
     """Enqueue one forward pass; cfg.workspace must point to workspace_size(cfg) bytes."""
     code = lib().muse_latent_moe_forward(ctypes.byref(cfg), _ptr(x), _ptr(W_router), _ptr(W_pool), _ptr(W_gate),
@@ -449,8 +468,8 @@ def quantize_int8_rows(src, codes=None, scales=None, stream=None, scale_rule: in
     import torch
     ptr, dtype, ld = _rows(src, "src")
     rows, K = src.shape
-    codes = torch.empty((rows, K), dtype=torch.int8, device=src.device) if codes is None else codes
-    scales = torch.empty(rows, dtype=torch.float32, device=src.device) if scales is None else scales
+    codes = _empty((rows, K), torch.int8, src.device, stream) if codes is None else codes
+    scales = _empty(rows, torch.float32, src.device, stream) if scales is None else scales
     _int8_operand(codes, scales, "int8")
     if codes.shape != src.shape:
         raise ValueError("codes must have the shape of src")
@@ -508,7 +527,7 @@ class Int8Linear:
             raise ValueError(f"tensors must be on {self._device}")
         dtype = None
         if out is None:
-            out = torch.empty((T, self.N), dtype=out_dtype, device=device)
+            out = _empty((T, self.N), out_dtype, device, stream)
             ptr, dtype, ld = out.data_ptr(), _float_types.get(out_dtype), self.N
         elif tuple(out.shape) != (T, self.N) or (out_dtype is not None and out.dtype != out_dtype):
             raise ValueError(f"out must be [{T}, {self.N}] of the output type")
@@ -695,7 +714,6 @@ class LatentMoE:
 
     def __call__(self, x, out=None, stream=None, topk_idx=None, topk_w=None, stage_events=None):
         """stage_events: optional ctypes array of launch_count + 1 cudaEvent_t handles."""
-        import torch
         T = x.shape[0]
         if T > self.T_max:
             raise ValueError(f"T={T} exceeds T_max={self.T_max}")
@@ -704,7 +722,7 @@ class LatentMoE:
         if stage_events is not None:
             cfg.stage_events = ctypes.cast(stage_events, ctypes.c_void_p)
         if out is None:
-            out = torch.empty((T, self.dims["D"]), dtype=x.dtype, device=x.device)
+            out = _empty((T, self.dims["D"]), x.dtype, x.device, stream)
         forward_checked(cfg, x, *self.operands(), out, stream)
         return out
 
@@ -727,7 +745,7 @@ class LatentMoE:
             cfg = Config.from_buffer_copy(few_config)
             cfg.T, cfg.topk_idx_out, cfg.topk_w_out = T, _ptr(topk_idx), _ptr(topk_w)
             if out is None:
-                out = torch.empty((T, self.dims["D"]), dtype=x.dtype, device=x.device)
+                out = _empty((T, self.dims["D"]), x.dtype, x.device, stream)
             code = lib().muse_latent_moe_few_tokens_checked(
                 ctypes.byref(cfg), ctypes.byref(tensor_desc(x)), *weights, ctypes.byref(tensor_desc(out)),
                 _stream_handle(stream))

@@ -24,8 +24,8 @@ from __future__ import annotations
 
 from typing import Dict, List, Optional, Sequence, Tuple
 
-from . import (EP_EXPERTS, EP_HOME, _ptr, block_config, ep_combine, ep_dispatch, ep_experts, ep_workspace_layout,
-               expert_operands, expert_weight_dims, projection_operand)
+from . import (EP_EXPERTS, EP_HOME, _empty, _ptr, block_config, ep_combine, ep_dispatch, ep_experts,
+               ep_workspace_layout, expert_operands, expert_weight_dims, projection_operand)
 
 
 class ExpertShard:
@@ -102,8 +102,8 @@ class ExpertShard:
         if R > self.rows_max:
             raise ValueError(f"{R} rows received, the expert workspace holds {self.rows_max}")
         L = self.dims["L"]
-        ret_y = torch.empty((R, L), dtype=self.act, device=recv_z.device)
-        ret_ss = torch.empty((R, L // 32), dtype=torch.float32, device=recv_z.device)
+        ret_y = _empty((R, L), self.act, recv_z.device, stream)
+        ret_ss = _empty((R, L // 32), torch.float32, recv_z.device, stream)
         cfg = self.config(self.T_max, self.ws_experts)
         wg, wu, wd = self.experts_args
         ep_experts(cfg, self.G, R, recv_z, recv_expert, wg, wu, wd, self.gamma_local, ret_y, ret_ss, stream)
@@ -112,10 +112,9 @@ class ExpertShard:
     def combine(self, x, back_y, back_ss, out=None, stream=None):
         """Per-expert norm, weighted combine and unpooler of this rank's tokens, from the rows
         of its send buffer that came back (the same workspace as the preceding dispatch)."""
-        import torch
         T = x.shape[0]
         if out is None:
-            out = torch.empty((T, self.dims["D"]), dtype=x.dtype, device=x.device)
+            out = _empty((T, self.dims["D"]), x.dtype, x.device, stream)
         if T == 0:
             return out
         cfg = self.config(T, self.ws_home)
