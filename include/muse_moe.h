@@ -410,7 +410,8 @@ MUSE_API muse_status muse_int8_linear_scaled(const void* x, int32_t x_dtype, int
  * expert outputs and the sublayer's f stay FP32, float32 workloads multiply in FP32 (not
  * TF32), NVFP4 experts read the latent and the hidden rows rounded to f16 once, and where bf16
  * weights multiply the latent, hidden rows or combined latent, these carry 16 significant
- * bits (two bf16 numbers each). It requires 16-bit or float32 activations (MUSE_ACT_NVFP4 is
+ * bits (two bf16 numbers each; an infinite weight may therefore give NaN where the forward
+ * gives an infinity). It requires 16-bit or float32 activations (MUSE_ACT_NVFP4 is
  * UNSUPPORTED); NVFP4 experts require L and I multiples of 256; int8 projections are
  * UNSUPPORTED. stage_events is ignored. cfg->workspace: device, 256-byte aligned,
  * muse_latent_moe_few_tokens_workspace_size bytes, a layout of its own; calls whose work

@@ -693,6 +693,11 @@ class LatentMoE:
         return (w["W_router"], one("W_pool", ("_codes", "_scales")), *experts, w["gamma"],
                 one("W_unpool", ("_codes", "_scales")))
 
+    @property
+    def experts(self):
+        """W_gate, W_up and W_down as the shape-checked entry points take them."""
+        return self.operands()[2:5]
+
     def _few(self):
         """Configuration and weight descriptors of few_tokens. They are made again only when something
         they say has changed (2 us to find out): a call of a few microseconds would otherwise

@@ -18,12 +18,15 @@
 // intermediates carry a token as two bf16 numbers, the rounded value and what rounding took off
 // (16 significant bits): up to four tokens in the MMA's eight columns, which would otherwise be
 // empty, more in a second MMA. The output's error is then its own rounding (1.7e-3 of its norm
-// instead of 3.7e-3; released norms 4.5e-3).
+// instead of 3.7e-3; released norms 4.5e-3). The sublayer's xn is one bf16 number, as in the
+// token-tiled forward. An infinite weight gives NaN where the second number is 0 or of the other
+// sign.
 //
 // Work split: the weight rows of a phase (of all distinct experts in a row) are divided evenly
 // over the CTAs by row, whatever the tile, so no SM waits for another's larger share; a row is
-// always summed whole, by the same warps in the same order, so its result does not depend on
-// the split.
+// always summed whole, by the same warps in the same order, so its sum does not depend on
+// the split. (The norms' sums of squares of y and f are one partial per CTA, added in CTA order: their
+// last bits follow the number of CTAs.)
 //
 // Roles (16 warps). Producers (4): three stream a CTA's weight rows through a ring of stages, up
 // to 32 rows x kc elements each, by 16-byte asynchronous copies (any row count and row start;
@@ -32,7 +35,8 @@
 // start the ring fills with the new phase's weights while the grid barrier is still pending
 // -- only the activations wait for it -- so DRAM stays busy through the barriers. (One bulk
 // copy per row piece, from one producer warp, instead: one token through the full-size bf16
-// layer in 331 us, against 171 with these copies at the time, 162 now.)
+// layer in 331 us, against 171 with these copies. This and the other comparisons in this file
+// are of two builds measured side by side, at the step where the choice was made.)
 // Products (8; with 16, NVFP4 120 us against 97): they split each stage along K. 16-bit weights go to the warp-level MMA (m16n8k16:
 // weight rows as A, the tokens as its 8 columns): lane (g, t) of a warp reads 16 consecutive
 // bytes of rows g and g + 8 and of token g, and the MMA's K order is that of these bytes in both
@@ -117,7 +121,10 @@ struct FewGeo {
     return xoff + x;
   }
 };
-constexpr uint32_t kFewXBytes = 74 * 1024;  // most that an expert's activation rows may take: 8 rows of 4096
+// Most that an expert's activation rows may take: 8 rows of 4096, what the ring can spare. With wider
+// latents or hidden rows and as many tokens they go through the stages, which then hold a quarter of
+// K: 29 experts of 4352 x 4352, eight tokens, 498 us (1.9 TB/s); of 4096 x 4096 233 (3.7 TB/s).
+constexpr uint32_t kFewXBytes = 74 * 1024;
 // The router's rows are few for a CTA (256 over 148): with at most kFewNarrow of them a stage
 // holds 2 or 4 times as much of K (FewArgs::narrow), or the ring would hold next to nothing (the
 // logits of the full-size layer were ready after 8.5 us, with DRAM idle, against 3).

@@ -99,9 +99,9 @@ struct Int8Load {
 
 // TPR threads per row (32, 128 or 256), which hold up to 32 values each, so that a row of up to 32 TPR
 // values is read once, all its loads in flight together; longer rows are read again for the
-// codes (from L2). Bound by reading the rows and writing the codes; five blocks an SM keep
-// enough loads in flight (8192 x 8192 bf16: 48 us, 83 with two). With the loads hidden the
-// conversion's instructions bound it (issue slots 68 % busy).
+// codes (from L2). Float32 rows are bound by reading them (4096 x 8192: 29.9 us, 4.7 TB/s from
+// DRAM). Of bf16 rows five blocks an SM keep enough loads in flight (8192 x 8192: 48-52 us, 83 with
+// two); no unit is full then (issue slots, the busiest, 68 %; a row's codes wait for its maximum).
 template <typename T, int TPR, bool ALIGNED>
 __global__ void __launch_bounds__(256, 5) k_quant_rows_int8(const T* __restrict__ src, int64_t ld, int rows, int K,
                                                          int8_t* __restrict__ codes, float* __restrict__ scales,
@@ -167,7 +167,9 @@ __global__ void __launch_bounds__(256, 5) k_quant_rows_int8(const T* __restrict_
 // added through shared memory.
 // FUSED (float rows, as many as eight warps can hold in registers): every CTA quantises the rows
 // itself while its ring fills, one launch less and no round trip through memory.
-// Bound by reading the weights: one row through 4096 x 8192 weights in 6.0 us (5.6 TB/s). From 17
+// Bound by reading the weights, in so short a time by the ramp of DRAM: one row through 4096 x 8192
+// weights in 10.3 us (3.3 TB/s), through 8192 x 8192 in 15.3 (4.4 TB/s); 7.7 us where 4096 x 8192
+// lie in L2 from the call before. From 17
 // rows on the split-K kernel is faster (64 rows: 10 us, against 27 here: every SM fetches all rows).
 constexpr int kInt8StreamRows = 16;
 constexpr int kInt8MaxStages = kFewMaxStages;  // (the ring's barriers are laid out for as many)
