@@ -693,6 +693,11 @@ class LatentMoE:
         return (w["W_router"], one("W_pool", ("_codes", "_scales")), *experts, w["gamma"],
                 one("W_unpool", ("_codes", "_scales")))
 
+    def _tensors(self):
+        """Every tensor of the block that a call reads."""
+        options = (self.w[n] for n in self.OPTIONS if self.w.get(n) is not None)
+        return (*options, *(t for o in self.operands() for t in (o if type(o) is tuple else (o,))))
+
     @property
     def experts(self):
         """W_gate, W_up and W_down as the shape-checked entry points take them."""
@@ -707,10 +712,8 @@ class LatentMoE:
                 for t in w.values()],
                list(w), list(self.dims.values()), dict(self.modes), ws is not None and (ws.data_ptr(), ws.numel()))
         if key != self._few_key:
-            operands = self.operands()
-            options = [w[n] for n in self.OPTIONS if w.get(n) is not None]
-            _one_device(*options, *(t for o in operands for t in (o if type(o) is tuple else (o,))))
-            self._few_call = self.config(min(self.T_max, FEW_TOKENS), ws), _weight_descs(*operands)
+            _one_device(*self._tensors(), *(() if ws is None else (ws,)))
+            self._few_call = self.config(min(self.T_max, FEW_TOKENS), ws), _weight_descs(*self.operands())
             self._few_key = key
         return self._few_call
 
@@ -722,13 +725,15 @@ class LatentMoE:
         T = x.shape[0]
         if T > self.T_max:
             raise ValueError(f"T={T} exceeds T_max={self.T_max}")
-        cfg = self.config(T, self.workspace)
-        cfg.topk_idx_out, cfg.topk_w_out = _ptr(topk_idx), _ptr(topk_w)
-        if stage_events is not None:
-            cfg.stage_events = ctypes.cast(stage_events, ctypes.c_void_p)
-        if out is None:
-            out = _empty((T, self.dims["D"]), x.dtype, x.device, stream)
-        forward_checked(cfg, x, *self.operands(), out, stream)
+        given = (t for t in (out, topk_idx, topk_w) if t is not None)
+        with _one_device(x, self.workspace, *given, *self._tensors()):
+            cfg = self.config(T, self.workspace)
+            cfg.topk_idx_out, cfg.topk_w_out = _ptr(topk_idx), _ptr(topk_w)
+            if stage_events is not None:
+                cfg.stage_events = ctypes.cast(stage_events, ctypes.c_void_p)
+            if out is None:
+                out = _empty((T, self.dims["D"]), x.dtype, x.device, stream)
+            forward_checked(cfg, x, *self.operands(), out, stream)
         return out
 
     def few_tokens(self, x, out=None, stream=None, topk_idx=None, topk_w=None):

@@ -121,6 +121,32 @@ def test_replacements_that_do_not_fit_are_refused():
 
 
 @pytest.mark.gpu
+def test_tensors_of_another_device_are_refused():
+    """Weights, options, workspaces, inputs and outputs alike, before anything reaches the library."""
+    w, x, weights = make(10)
+    layer = layer_of(w, weights)
+    want = both(layer, x)
+
+    def refused(**kw):
+        for call in (layer.few_tokens, layer):
+            with pytest.raises(ValueError):
+                call(kw.get("x", x), **{n: t for n, t in kw.items() if n != "x"})
+    for name in ("W_router", "W_pool", "W_down", "gamma", "router_bias", "residual_gate"):
+        kept, layer.w[name] = layer.w[name], layer.w[name].cpu()
+        refused()
+        layer.w[name] = kept
+    refused(x=x.cpu())
+    refused(out=torch.empty_like(x).cpu())
+    refused(topk_idx=torch.empty(w.T, w.k, dtype=torch.int32))
+    refused(topk_w=torch.empty(w.T, w.k))
+    kept = layer.workspace, layer.few_workspace
+    layer.workspace, layer.few_workspace = (t.cpu() for t in kept)
+    refused()
+    layer.workspace, layer.few_workspace = kept
+    assert all(torch.equal(a, b) for a, b in zip(both(layer, x), want))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("how", ["attribute", "storage"])
 @pytest.mark.parametrize("T", [3, 40])
 def test_replaced_weights_of_a_product_are_used(T, how):
